@@ -240,6 +240,88 @@ int kda_chunk_fwd_noalloc(const kda_problem* p, kda_dtype dtype,
                           const float* initial_state, void* o, float* final_state,
                           uint32_t* device_status, void* stream);
 
+/* ---- operators beside the KDA scan ------------------------------------------------------------------
+ * What a token mixer with one decay per head needs: rotary positions over (time, height, width), linear
+ * attention with that decay (whole sequences, gradients, single tokens), and the layer norm in front of the
+ * mixer.  The pages have no counterpart.  They follow the conventions above; of a kda_problem they use the shape
+ * (B, H, dk = dv of 64 or 128, and the token count of text_len and the grid); its conv and scan options must be
+ * valid and have no effect, KDA_FLAG_REUSE_RECORDS and KDA_FLAG_QKV_F16 are rejected, and B * H may be at most
+ * 65535.  The aliasing rule is checked: an output that shares bytes with an input or another output returns
+ * KDA_ERR_INVALID_ARG, except where a call says that it works in place.  Results do not depend on timing: no
+ * sum's order varies between runs. */
+
+/* Interleaved pairs: pair j of a head is (2j, 2j+1) instead of (j, j + d/2). */
+#define KDA_ROPE_INTERLEAVED 1u
+typedef struct {
+  int32_t pairs_t, pairs_h, pairs_w;   /* pairs turned by the time, height and width position, in this order
+                                          from pair 0; each >= 0, together d/2 */
+  uint32_t flags;                      /* KDA_ROPE_* */
+} kda_rope;
+
+/* Rotary positions on q and k [B, N, H, d] of dtype: pair (a, b) = pair j of every head of token n becomes
+ *   (a cos w - b sin w, a sin w + b cos w),   w = position[n][axis(j)] * inv_freq[j].
+ * inv_freq: [d/2] fp32 device values.  positions: [B, N, 3] int32 (time, height, width; any sign), or NULL for
+ * the positions of the token stream: text token i at (i, i, i), visual token (t, h, w) at (text_len + t,
+ * text_len + h, text_len + w).  Angles are reduced in fp64, so far positions keep the accuracy of near ones.
+ * k and k_out may both be NULL (one tensor only).  Works in place with q_out = q, k_out = k (exactly).
+ * Returns a kda_status. */
+int kda_rope_fwd(const kda_problem* p, const kda_rope* rope, kda_dtype dtype,
+                 const void* q, const void* k, const float* inv_freq, const int32_t* positions,
+                 void* q_out, void* k_out, void* stream);
+
+/* Its backward pass: gradients of q and k from those of q_out and k_out (the turn back by the same angles).
+ * Same arguments; dq and dk may be d_q_out and d_k_out. */
+int kda_rope_bwd(const kda_problem* p, const kda_rope* rope, kda_dtype dtype,
+                 const void* d_q_out, const void* d_k_out, const float* inv_freq, const int32_t* positions,
+                 void* dq, void* dk, void* stream);
+
+/* Layer norm over the last axis of x [rows, cols]: y = (x - mean) * rstd * weight + bias with
+ * rstd = (mean of (x - mean)^2 + eps)^(-1/2), statistics in fp32.  x and y have dtype; weight and bias are
+ * [cols] fp32 or NULL (1 and 0); mean and rstd, [rows] fp32 or NULL, receive the statistics that the backward
+ * pass takes.  cols up to 16384 (beyond: KDA_ERR_UNSUPPORTED); rows may be 0.  Returns a kda_status. */
+int kda_layernorm_fwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* x, const float* weight,
+                      const float* bias, float eps, void* y, float* mean, float* rstd, void* stream);
+
+/* Its backward pass: dx [rows, cols] of dtype from dy, x and the forward pass's mean and rstd, and the sums over
+ * the rows d_weight, d_bias [cols] fp32 (either may be NULL).  The workspace is
+ * kda_layernorm_bwd_workspace_bytes(rows, cols) bytes, 256-byte aligned.  Returns a kda_status. */
+size_t kda_layernorm_bwd_workspace_bytes(int64_t rows, int32_t cols);
+int kda_layernorm_bwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* dy, const void* x,
+                      const float* weight, const float* mean, const float* rstd, void* dx, float* d_weight,
+                      float* d_bias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Linear attention with a fixed decay per head, per (batch item, head):
+ *   S_t = exp(log_decay_h) S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t      (no scale on q)
+ * with S_{-1} = initial_state (or 0).  q, k, v, o: [B, N, H, d] of dtype; log_decay: [H] fp32, <= 0 (0 forgets
+ * nothing, -inf keeps the token alone); initial_state, final_state: [B, H, d, d] fp32 or NULL.
+ * lengths: [B] int32 or NULL (N each).  Item b's sequence is its first lengths[b] tokens (clamped to 0..N): what
+ * q, k, v hold behind them is not used, whatever it is, o is zero there, and final_state is the state after the
+ * item's own last token.  Inputs within the sequences must be finite.  The workspace is
+ * kda_linear_workspace_bytes(p, dtype) bytes, 256-byte aligned.  Returns a kda_status. */
+size_t kda_linear_workspace_bytes(const kda_problem* p, kda_dtype dtype);
+int kda_linear_fwd(const kda_problem* p, kda_dtype dtype,
+                   const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,
+                   const float* initial_state, void* o, float* final_state,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its backward pass: the gradients of sum(d_o * o) + sum(d_final_state * final_state) with respect to q, k, v and
+ * initial_state (the decay is a constant).  d_final_state may be NULL (zero), d_initial_state NULL (not written).
+ * dq, dk, dv are zero behind an item's length, and what d_o holds there is not used.  The workspace is
+ * kda_linear_bwd_workspace_bytes(p, dtype) bytes, 256-byte aligned.  Returns a kda_status. */
+size_t kda_linear_bwd_workspace_bytes(const kda_problem* p, kda_dtype dtype);
+int kda_linear_bwd(const kda_problem* p, kda_dtype dtype,
+                   const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,
+                   const float* initial_state, const void* d_o, const float* d_final_state,
+                   void* dq, void* dk, void* dv, float* d_initial_state,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of the recurrence for every (batch item, head): a problem of N = 1 (otherwise KDA_ERR_INVALID_ARG).
+ * state_out = exp(log_decay) state_in + k v^T, o = state_out^T q.  Works in place with state_out = state_in.
+ * No workspace.  Returns a kda_status. */
+int kda_linear_step(const kda_problem* p, kda_dtype dtype,
+                    const void* q, const void* k, const void* v, const float* log_decay,
+                    const float* state_in, void* o, float* state_out, void* stream);
+
 /* Self-test of the bounded device waits; the pages have no counterpart.  Every wait of the kernels
  * (for an asynchronous copy, a tensor-core product or another warp) gives up after a time limit and
  * records KDA_ERR_TIMEOUT instead of hanging the GPU; this call makes one such wait run out on purpose

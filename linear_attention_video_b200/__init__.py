@@ -34,10 +34,14 @@ KDA_DT_BF16, KDA_DT_F32 = 0, 1
 KDA_FLAG_VIS_CAUSAL_T = 1
 KDA_FLAG_REUSE_RECORDS = 2
 KDA_FLAG_QKV_F16 = 4
+KDA_ROPE_INTERLEAVED = 1
 
 EXPORTS = ("kda_tokens", "kda_workspace_bytes", "kda_shortconv_fwd", "kda_chunk_fwd", "kda_fwd",
            "kda_chunk_fwd_noalloc", "kda_fwd_host_workspace_bytes", "kda_fwd_host", "kda_bwd_workspace_bytes",
-           "kda_bwd", "kda_selftest_wait_timeout", "kda_read_status", "kda_status_str", "kda_last_launch_count")
+           "kda_bwd", "kda_rope_fwd", "kda_rope_bwd", "kda_layernorm_fwd", "kda_layernorm_bwd_workspace_bytes",
+           "kda_layernorm_bwd", "kda_linear_workspace_bytes", "kda_linear_fwd", "kda_linear_bwd_workspace_bytes",
+           "kda_linear_bwd", "kda_linear_step", "kda_selftest_wait_timeout", "kda_read_status", "kda_status_str",
+           "kda_last_launch_count")
 
 
 class kda_problem(ctypes.Structure):
@@ -47,6 +51,11 @@ class kda_problem(ctypes.Structure):
                 ("text_k", ctypes.c_int32),
                 ("vis_kt", ctypes.c_int32), ("vis_kh", ctypes.c_int32), ("vis_kw", ctypes.c_int32),
                 ("chunk", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class kda_rope(ctypes.Structure):
+    _fields_ = [("pairs_t", ctypes.c_int32), ("pairs_h", ctypes.c_int32), ("pairs_w", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
 
 
 _vp, _sz, _i, _pp = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.POINTER(kda_problem)
@@ -70,6 +79,26 @@ _lib.kda_bwd_workspace_bytes.argtypes = [_pp, _i]
 _lib.kda_bwd_workspace_bytes.restype = _sz
 _lib.kda_bwd.argtypes = [_pp, _i] + [_vp] * 19 + [_sz, _vp]
 _lib.kda_bwd.restype = _i
+_lib.kda_rope_fwd.argtypes = [_pp, ctypes.POINTER(kda_rope), _i] + [_vp] * 7
+_lib.kda_rope_fwd.restype = _i
+_lib.kda_rope_bwd.argtypes = _lib.kda_rope_fwd.argtypes
+_lib.kda_rope_bwd.restype = _i
+_lib.kda_layernorm_fwd.argtypes = [ctypes.c_int64, ctypes.c_int32, _i] + [_vp] * 3 + [ctypes.c_float] + [_vp] * 4
+_lib.kda_layernorm_fwd.restype = _i
+_lib.kda_layernorm_bwd_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32]
+_lib.kda_layernorm_bwd_workspace_bytes.restype = _sz
+_lib.kda_layernorm_bwd.argtypes = [ctypes.c_int64, ctypes.c_int32, _i] + [_vp] * 9 + [_sz, _vp]
+_lib.kda_layernorm_bwd.restype = _i
+_lib.kda_linear_workspace_bytes.argtypes = [_pp, _i]
+_lib.kda_linear_workspace_bytes.restype = _sz
+_lib.kda_linear_fwd.argtypes = [_pp, _i] + [_vp] * 9 + [_sz, _vp]
+_lib.kda_linear_fwd.restype = _i
+_lib.kda_linear_bwd_workspace_bytes.argtypes = [_pp, _i]
+_lib.kda_linear_bwd_workspace_bytes.restype = _sz
+_lib.kda_linear_bwd.argtypes = [_pp, _i] + [_vp] * 13 + [_sz, _vp]
+_lib.kda_linear_bwd.restype = _i
+_lib.kda_linear_step.argtypes = [_pp, _i] + [_vp] * 8
+_lib.kda_linear_step.restype = _i
 _lib.kda_selftest_wait_timeout.argtypes = [_pp, _i] + [_vp] * 7 + [_sz, ctypes.c_int32, ctypes.c_uint32, _vp]
 _lib.kda_selftest_wait_timeout.restype = _i
 _lib.kda_read_status.argtypes = [_vp, _vp]
@@ -93,6 +122,11 @@ def problem(B, H, d, text_len, grid, text_k=4, vis_k=(3, 3, 3), chunk=64, vis_ca
              | (KDA_FLAG_QKV_F16 if qkv_f16 else 0))
     return kda_problem(B, H, d, d if dv is None else dv, text_len, T, Hg, Wg, text_k,
                        vis_k[0], vis_k[1], vis_k[2], chunk, flags)
+
+
+def rope(pairs, interleaved=False) -> kda_rope:
+    """Rotary layout: pairs of a head turned by the (time, height, width) position, together d/2."""
+    return kda_rope(*pairs, KDA_ROPE_INTERLEAVED if interleaved else 0)
 
 
 def _dt(dtype) -> int:
@@ -336,6 +370,150 @@ def kda_bwd(p, q, k, v, log_alpha, beta, w_text, w_vis, d_o, dq, dk, dv, d_log_a
                         _ptr(dk_), _ptr(dv_), _ptr(d_log_alpha), _ptr(d_beta), _ptr(d_w_text), _ptr(d_w_vis),
                         _ptr(d_initial_state), _ptr(workspace), nbytes, _stream(stream)),
            "kda_bwd")
+
+
+# ---------------------------------------------------------------------------
+# operators beside the KDA scan: rotary positions, layer norm, linear attention with a decay per head
+# ---------------------------------------------------------------------------
+def _rope_call(where, p, r, q, k, inv_freq, q_out, k_out, positions, stream):
+    B, N, H, d, _ = _dims(p)
+    a = _Args(where)
+    for n, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)):
+        a.add(n, t, B * N * H * d, (q.dtype,))
+    a.add("inv_freq", inv_freq, d // 2, (torch.float32,))
+    a.add("positions", positions, B * N * 3, (torch.int32,)).check_devices()
+    _check(getattr(_lib, where)(ctypes.byref(p), ctypes.byref(r), _dt(q.dtype), _ptr(q), _ptr(k), _ptr(inv_freq),
+                                _ptr(positions), _ptr(q_out), _ptr(k_out), _stream(stream)), where)
+
+
+def kda_rope_fwd(p, r, q, k, inv_freq, q_out, k_out, positions=None, stream=None):
+    """Rotary positions on q and k (k and k_out may be None); q_out and k_out may be q and k."""
+    _rope_call("kda_rope_fwd", p, r, q, k, inv_freq, q_out, k_out, positions, stream)
+
+
+def kda_rope_bwd(p, r, d_q_out, d_k_out, inv_freq, dq, dk, positions=None, stream=None):
+    """Gradients of q and k from those of kda_rope_fwd's outputs."""
+    _rope_call("kda_rope_bwd", p, r, d_q_out, d_k_out, inv_freq, dq, dk, positions, stream)
+
+
+def _rows_cols(where, x):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.shape[-1] < 1:
+        raise KdaError(KDA_ERR_INVALID_ARG, f"{where}: x must be a torch tensor with a last axis to normalise")
+    return x.numel() // x.shape[-1], x.shape[-1]
+
+
+def kda_layernorm_fwd(x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=None, stream=None):
+    """Layer norm over x's last axis; weight, bias, mean and rstd are fp32 or None."""
+    rows, cols = _rows_cols("kda_layernorm_fwd", x)
+    f32 = (torch.float32,)
+    a = _Args("kda_layernorm_fwd").add("x", x, rows * cols, (x.dtype,)).add("y", y, rows * cols, (x.dtype,))
+    a.add("weight", weight, cols, f32).add("bias", bias, cols, f32)
+    a.add("mean", mean, rows, f32).add("rstd", rstd, rows, f32).check_devices()
+    _check(_lib.kda_layernorm_fwd(rows, cols, _dt(x.dtype), _ptr(x), _ptr(weight), _ptr(bias), eps, _ptr(y),
+                                  _ptr(mean), _ptr(rstd), _stream(stream)), "kda_layernorm_fwd")
+
+
+def kda_layernorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    return _lib.kda_layernorm_bwd_workspace_bytes(rows, cols)
+
+
+def alloc_layernorm_bwd_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    n = kda_layernorm_bwd_workspace_bytes(rows, cols)
+    if n == 0:
+        raise KdaError(KDA_ERR_INVALID_ARG, "kda_layernorm_bwd_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _workspace_arg(a, workspace, nbytes):
+    if workspace is not None and not isinstance(workspace, int):
+        a.add("workspace", workspace, 1, (workspace.dtype,), at_least=True)
+        if workspace.numel() * workspace.element_size() < nbytes:
+            a.fail(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, fewer than the "
+                   f"{nbytes} passed")
+    return a
+
+
+def kda_layernorm_bwd(dy, x, mean, rstd, dx, workspace, weight=None, d_weight=None, d_bias=None, stream=None,
+                      workspace_bytes=None):
+    """Gradients of kda_layernorm_fwd: dx, and the sums d_weight and d_bias (either may be None)."""
+    rows, cols = _rows_cols("kda_layernorm_bwd", x)
+    nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    f32 = (torch.float32,)
+    a = _Args("kda_layernorm_bwd")
+    for n, t in (("dy", dy), ("x", x), ("dx", dx)):
+        a.add(n, t, rows * cols, (x.dtype,))
+    a.add("mean", mean, rows, f32).add("rstd", rstd, rows, f32)
+    for n, t in (("weight", weight), ("d_weight", d_weight), ("d_bias", d_bias)):
+        a.add(n, t, cols, f32)
+    _workspace_arg(a, workspace, nbytes).check_devices()
+    _check(_lib.kda_layernorm_bwd(rows, cols, _dt(x.dtype), _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
+                                  _ptr(dx), _ptr(d_weight), _ptr(d_bias), _ptr(workspace), nbytes, _stream(stream)),
+           "kda_layernorm_bwd")
+
+
+def kda_linear_workspace_bytes(p: kda_problem, dtype) -> int:
+    return _lib.kda_linear_workspace_bytes(ctypes.byref(p), _dt(dtype))
+
+
+def alloc_linear_workspace(p: kda_problem, dtype, device="cuda") -> torch.Tensor:
+    n = kda_linear_workspace_bytes(p, dtype)
+    if n == 0:
+        raise KdaError(KDA_ERR_INVALID_ARG, "kda_linear_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kda_linear_bwd_workspace_bytes(p: kda_problem, dtype) -> int:
+    return _lib.kda_linear_bwd_workspace_bytes(ctypes.byref(p), _dt(dtype))
+
+
+def alloc_linear_bwd_workspace(p: kda_problem, dtype, device="cuda") -> torch.Tensor:
+    n = kda_linear_bwd_workspace_bytes(p, dtype)
+    if n == 0:
+        raise KdaError(KDA_ERR_INVALID_ARG, "kda_linear_bwd_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _linear_args(where, p, q, k, v, log_decay, lengths, acts, states, workspace=None, nbytes=0):
+    B, N, H, d, _ = _dims(p)
+    a = _Args(where)
+    for n, t in (("q", q), ("k", k), ("v", v)) + acts:
+        a.add(n, t, B * N * H * d, (q.dtype,))
+    a.add("log_decay", log_decay, H, (torch.float32,)).add("lengths", lengths, B, (torch.int32,))
+    for n, t in states:
+        a.add(n, t, B * H * d * d, (torch.float32,))
+    _workspace_arg(a, workspace, nbytes).check_devices()
+
+
+def kda_linear_fwd(p, q, k, v, log_decay, o, workspace, lengths=None, initial_state=None, final_state=None,
+                   stream=None, workspace_bytes=None):
+    """Linear attention with a fixed decay per head over whole sequences."""
+    nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _linear_args("kda_linear_fwd", p, q, k, v, log_decay, lengths, (("o", o),),
+                 (("initial_state", initial_state), ("final_state", final_state)), workspace, nbytes)
+    _check(_lib.kda_linear_fwd(ctypes.byref(p), _dt(q.dtype), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                               _ptr(lengths), _ptr(initial_state), _ptr(o), _ptr(final_state), _ptr(workspace),
+                               nbytes, _stream(stream)), "kda_linear_fwd")
+
+
+def kda_linear_bwd(p, q, k, v, log_decay, d_o, dq, dk, dv, workspace, lengths=None, initial_state=None,
+                   d_final_state=None, d_initial_state=None, stream=None, workspace_bytes=None):
+    """Gradients of kda_linear_fwd with respect to q, k, v and initial_state."""
+    nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _linear_args("kda_linear_bwd", p, q, k, v, log_decay, lengths, (("d_o", d_o), ("dq", dq), ("dk", dk), ("dv", dv)),
+                 (("initial_state", initial_state), ("d_final_state", d_final_state),
+                  ("d_initial_state", d_initial_state)), workspace, nbytes)
+    _check(_lib.kda_linear_bwd(ctypes.byref(p), _dt(q.dtype), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                               _ptr(lengths), _ptr(initial_state), _ptr(d_o), _ptr(d_final_state), _ptr(dq),
+                               _ptr(dk), _ptr(dv), _ptr(d_initial_state), _ptr(workspace), nbytes, _stream(stream)),
+           "kda_linear_bwd")
+
+
+def kda_linear_step(p, q, k, v, log_decay, state_in, o, state_out, stream=None):
+    """One token of the recurrence for every batch item and head; state_out may be state_in."""
+    _linear_args("kda_linear_step", p, q, k, v, log_decay, None, (("o", o),),
+                 (("state_in", state_in), ("state_out", state_out)))
+    _check(_lib.kda_linear_step(ctypes.byref(p), _dt(q.dtype), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                _ptr(state_in), _ptr(o), _ptr(state_out), _stream(stream)), "kda_linear_step")
 
 
 def kda_selftest_wait_timeout(p, q, k, v, log_alpha, beta, o, workspace, stage, wait_us, stream=None):

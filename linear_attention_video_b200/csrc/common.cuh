@@ -74,6 +74,89 @@ cudaError_t launch_chunk_tc(const Dims& d, bool in_f16, const void* q, const voi
                             void* ws, uint32_t* status, cudaStream_t s, int* launches, int fault = 0,
                             uint64_t wait_ns = kWaitNs);
 
+// Rotary positions (rope.cu): tokens = B * N of the flattened [B, N, H, d] tensors x[0..n_tensors).
+struct RopeArgs {
+  const void* x[2];
+  void* y[2];
+  const float* inv_freq;
+  const int32_t* positions;   // [tokens][3], or NULL: from the text + grid layout
+  int64_t tokens, N, text;
+  int H, Hg, Wg, n_tensors, pairs_t, pairs_h;
+  bool inverse;
+};
+cudaError_t launch_rope(const RopeArgs& a, kda_dtype dt, int d, bool interleaved, cudaStream_t s, int* launches);
+
+// Layer norm (layernorm.cu).
+constexpr int kNormMaxCols = 16384;
+struct NormFwdArgs {
+  const void* x;
+  const float *weight, *bias;
+  void* y;
+  float *mean, *rstd;
+  int64_t rows;
+  int cols;
+  float eps;
+};
+struct NormBwdArgs {
+  const void *dy, *x;
+  const float *weight, *mean, *rstd;
+  void* dx;
+  float* parts;   // partial sums of the weight's and the bias's gradient, NULL if neither is wanted
+  int64_t rows;
+  int cols;
+};
+cudaError_t launch_norm_fwd(const NormFwdArgs& a, kda_dtype dt, cudaStream_t s, int* launches);
+size_t norm_bwd_parts(int64_t rows, int cols);
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, kda_dtype dt, float* dw, float* db, cudaStream_t s, int* launches);
+
+// Linear attention with a decay per head (linear.cu).
+struct LinLocalArgs {
+  const void *x, *y;
+  const float* log_decay;
+  const int32_t* lengths;
+  float* local;      // [B][H][n_seg][D][D]
+  int64_t N;
+  int H, n_seg;
+  bool reverse;      // weights towards the segment's first token instead of its last
+};
+struct LinScanArgs {
+  float* states;           // [B][H][n_seg][D][D], in place
+  const float* initial;    // [B][H][D][D] or NULL (zero)
+  float* final;            // [B][H][D][D] or NULL
+  const float* log_decay;
+  const int32_t* lengths;
+  int64_t N, dd;
+  int seg, H, n_seg;
+  bool reverse;
+};
+struct LinMapArgs {
+  const void *a, *b, *c;
+  void* out;
+  const float *states, *initial;   // what enters each segment; with one segment, `initial` itself
+  const float* log_decay;
+  const int32_t* lengths;
+  int64_t N;
+  int H, n_seg;
+  bool reverse, transposed;
+};
+struct LinStepArgs {
+  const void *q, *k, *v;
+  const float *log_decay, *state_in;
+  void* o;
+  float* state_out;
+  int H;
+};
+size_t linear_fwd_scratch(const Dims& d);
+size_t linear_bwd_scratch(const Dims& d);
+cudaError_t launch_linear_fwd(const Dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
+                              const float* log_decay, const int32_t* lengths, const float* S0, void* o, float* SN,
+                              void* scratch, cudaStream_t s, int* launches);
+cudaError_t launch_linear_bwd(const Dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
+                              const float* log_decay, const int32_t* lengths, const float* S0, const void* d_o,
+                              const float* dSN, void* dq, void* dk, void* dv, float* dS0, void* scratch,
+                              cudaStream_t s, int* launches);
+cudaError_t launch_linear_step(const Dims& d, kda_dtype dt, const LinStepArgs& a, cudaStream_t s, int* launches);
+
 // Host-side validation (kda_api.cu), returning a kda_status.
 int validate_problem(const kda_problem* p, kda_dtype dt, Dims* d);
 int validate_scan_pointers(const void* q, const void* k, const void* v, const void* la, const void* beta, const void* o,

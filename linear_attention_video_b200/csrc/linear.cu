@@ -1,0 +1,481 @@
+// Linear attention with a fixed decay per head: S_t = lam S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+//
+// The token axis is cut into segments of L tokens.  With s0 the first token of i's segment, n its tokens and S
+// the state entering it,
+//   o_i  = lam^(i-s0+1) S^T q_i + sum_{s0 <= j <= i} lam^(i-j) (q_i . k_j) v_j
+// and with G the gradient that reaches the state leaving the segment
+//   dq_i = lam^(i-s0+1) S do_i     + sum_{j <= i} lam^(i-j) (do_i . v_j) k_j
+//   dk_j = lam^(s0+n-1-j) G v_j    + sum_{i >= j} lam^(i-j) (v_j . do_i) q_i
+//   dv_j = lam^(s0+n-1-j) G^T k_j  + sum_{i >= j} lam^(i-j) (k_j . q_i) do_i
+// so all four are one map over (a, b, c, state) in one of two directions:
+//   out_i = lam^e(i) X^(T) a_i + sum_j lam^|i-j| (a_i . b_j) c_j.
+// Three launches: every segment's own contribution sum_t w_t x_t y_t^T to the state behind it (before it, for
+// G); the recurrence over segments, element by element; the map, whose tiles are then independent.
+//
+// The matrix products here run on mma.sync in tf32 with each fp32 operand split into two terms (three products,
+// 2^-22 relative), so fp32 problems keep fp32 accuracy; bf16 inputs are exact in tf32 and need one term.
+// Decays are lam^n = exp(n log lam) of whole n >= 0: never above 1, so nothing overflows however fast a head
+// forgets, and the fp32 error of n log lam, 2^-25 |n log lam|, is largest beside e^-1.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace kda {
+namespace {
+
+// lam^n; 1 at n = 0 whatever the decay.
+__device__ __forceinline__ float decay_pow(float log_decay, int64_t n) {
+  return n == 0 ? 1.f : expf((float)n * log_decay);
+}
+__device__ __forceinline__ int64_t item_tokens(const int32_t* lengths, int b, int64_t N) {
+  if (!lengths) return N;
+  const int64_t n = lengths[b];
+  return n < 0 ? 0 : (n > N ? N : n);
+}
+
+// ---------------------------------------------------------------------------
+// tf32 products
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+// x = hi + lo to 22 bits.
+__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
+  hi = tf32(x);
+  lo = tf32(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// d += A B with A and B in one (exact) or two (split) terms each.
+template <bool SplitA, bool SplitB>
+__device__ __forceinline__ void mma_terms(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float b0,
+                                          float b1) {
+  uint32_t bh[2], bl[2];
+  if constexpr (SplitB) {
+    split(b0, bh[0], bl[0]);
+    split(b1, bh[1], bl[1]);
+    mma8(d, ah, bl);
+  } else {
+    bh[0] = __float_as_uint(b0);
+    bh[1] = __float_as_uint(b1);
+  }
+  if constexpr (SplitA) mma8(d, al, bh);
+  mma8(d, ah, bh);
+}
+template <bool Split>
+__device__ __forceinline__ void a_terms(const float (&x)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (Split) split(x[i], hi[i], lo[i]);
+    else hi[i] = __float_as_uint(x[i]), lo[i] = 0u;
+  }
+}
+
+template <typename T> __device__ __forceinline__ float4 load4(const T* p);
+template <> __device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(&u)[0]);
+  const float2 b = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(&u)[1]);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+
+constexpr int TK = 32;       // tokens per shared-memory tile
+constexpr int TQ = 64;       // output rows per CTA
+constexpr int kSeg = 256;    // tokens per segment
+
+// ---------------------------------------------------------------------------
+// a segment's own contribution: local[x][y] = sum_t w_t x_t y_t^T
+// w_t = lam^(s0+n-1-t) (state behind it), or lam^(t-s0+1) (gradient before it)
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(256) lin_local_kernel(LinLocalArgs a) {
+  constexpr int LD = D + 8;            // rows 8 banks apart: A and B fragments without conflicts
+  constexpr int RG = D / 16, CG = 8 / RG, NT = D / CG / 8;
+  constexpr bool kF32 = sizeof(T) == 4;
+  __shared__ float xs[TK * LD], ys[TK * LD];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int64_t s0 = (int64_t)seg * kSeg, end = min(item_tokens(a.lengths, b, a.N), s0 + kSeg);
+  const float ld = a.log_decay[h];
+  const int64_t stride = (int64_t)a.H * D;
+  const T* x = static_cast<const T*>(a.x) + (int64_t)b * a.N * stride + (int64_t)h * D;
+  const T* y = static_cast<const T*>(a.y) + (int64_t)b * a.N * stride + (int64_t)h * D;
+  const int m0 = (warp % RG) * 16, n0 = (warp / RG) * (D / CG);
+  float acc[NT][4] = {};
+  for (int64_t t0 = s0; t0 < end; t0 += TK) {
+    __syncthreads();
+    for (int i = tid; i < TK * D / 4; i += 256) {
+      const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+      float4 fx = make_float4(0.f, 0.f, 0.f, 0.f), fy = fx;
+      if (t0 + r < end) {
+        fx = load4<T>(x + (t0 + r) * stride + c);
+        fy = load4<T>(y + (t0 + r) * stride + c);
+        const float w = decay_pow(ld, a.reverse ? t0 + r - s0 + 1 : end - 1 - t0 - r);
+        fy.x *= w; fy.y *= w; fy.z *= w; fy.w *= w;
+      }
+      *reinterpret_cast<float4*>(xs + r * LD + c) = fx;
+      *reinterpret_cast<float4*>(ys + r * LD + c) = fy;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k8 = 0; k8 < TK / 8; ++k8) {
+      const float* xr = xs + (k8 * 8 + t) * LD + m0 + g;
+      const float av[4] = {xr[0], xr[8], xr[4 * LD], xr[4 * LD + 8]};
+      uint32_t ah[4], al[4];
+      a_terms<kF32>(av, ah, al);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float* yr = ys + (k8 * 8 + t) * LD + n0 + n * 8 + g;
+        mma_terms<kF32, true>(acc[n], ah, al, yr[0], yr[4 * LD]);
+      }
+    }
+  }
+  float* out = a.local + (((int64_t)b * a.H + h) * a.n_seg + seg) * D * D;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    store2(out + (m0 + g) * D + n0 + n * 8 + 2 * t, acc[n][0], acc[n][1]);
+    store2(out + (m0 + g + 8) * D + n0 + n * 8 + 2 * t, acc[n][2], acc[n][3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// recurrence over segments, in place: local contributions become what enters each segment
+// ---------------------------------------------------------------------------
+// The decay of a whole segment multiplies a state again and again, so its fp32 rounding would add up; it is kept
+// in two fp32 terms of the fp64 power.
+struct Factor { float hi, lo; };
+__device__ __forceinline__ Factor segment_factor(float log_decay, int64_t n) {
+  const double f = n == 0 ? 1.0 : exp((double)n * (double)log_decay);
+  const float hi = (float)f;
+  return {hi, (float)(f - (double)hi)};
+}
+
+__global__ void __launch_bounds__(128) lin_scan_kernel(LinScanArgs a) {
+  const int bh = blockIdx.y, h = bh % a.H, b = bh / a.H;
+  const int64_t e = ((int64_t)blockIdx.x * 128 + threadIdx.x) * 4;   // element of the D x D state
+  const int64_t dd = a.dd, len = item_tokens(a.lengths, b, a.N);
+  const float ld = a.log_decay[h];
+  const int64_t last = len / a.seg;   // the segment that holds the end, if it is not whole
+  const Factor whole = segment_factor(ld, a.seg), part = segment_factor(ld, len % a.seg);
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.initial) S = *reinterpret_cast<const float4*>(a.initial + bh * dd + e);
+  float* p = a.states + (int64_t)bh * a.n_seg * dd + e;
+  constexpr int U = 4;
+  for (int c0 = 0; c0 < a.n_seg; c0 += U) {
+    float4 loc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u < a.n_seg)
+        loc[u] = *reinterpret_cast<const float4*>(p + (int64_t)(a.reverse ? a.n_seg - 1 - c0 - u : c0 + u) * dd);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c0 + u >= a.n_seg) break;
+      const int c = a.reverse ? a.n_seg - 1 - c0 - u : c0 + u;
+      *reinterpret_cast<float4*>(p + (int64_t)c * dd) = S;
+      if (c > last) continue;   // behind the end: no tokens
+      const Factor f = c == last ? part : whole;
+      S.x = fmaf(f.hi, S.x, fmaf(f.lo, S.x, loc[u].x));
+      S.y = fmaf(f.hi, S.y, fmaf(f.lo, S.y, loc[u].y));
+      S.z = fmaf(f.hi, S.z, fmaf(f.lo, S.z, loc[u].z));
+      S.w = fmaf(f.hi, S.w, fmaf(f.lo, S.w, loc[u].w));
+    }
+  }
+  if (a.final) *reinterpret_cast<float4*>(a.final + bh * dd + e) = S;
+}
+
+// ---------------------------------------------------------------------------
+// the map: out_i = lam^e(i) X^(T) a_i + sum_j lam^|i-j| (a_i . b_j) c_j over i's segment
+// ---------------------------------------------------------------------------
+template <int D> struct MapSmem {
+  static constexpr int LDA = D + 8;   // a, b: pairs of columns read as 8 bytes, rows 8 banks apart
+  static constexpr int LDC = D + 4;   // c: rows 2t read by lane t, 8 banks apart
+  static constexpr int floats = TQ * LDA + TK * LDA + TK * LDC + kSeg;
+  static constexpr int bytes = floats * (int)sizeof(float);
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(128) lin_map_kernel(LinMapArgs a) {
+  using L = MapSmem<D>;
+  constexpr int LDA = L::LDA, LDC = L::LDC, NT = D / 8;
+  constexpr bool kF32 = sizeof(T) == 4;
+  extern __shared__ float sm[];
+  float* as = sm;
+  float* bs = as + TQ * LDA;
+  float* cs = bs + TK * LDA;
+  float* pw = cs + TK * LDC;   // lam^n, n < kSeg
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int64_t i0 = (int64_t)blockIdx.x * TQ;
+  const int seg = (int)(i0 / kSeg);
+  const int64_t s0 = (int64_t)seg * kSeg, len = item_tokens(a.lengths, b, a.N), end = min(len, s0 + kSeg);
+  const float ld = a.log_decay[h];
+  const int64_t stride = (int64_t)a.H * D, off = (int64_t)b * a.N * stride + (int64_t)h * D;
+  const T *pa = static_cast<const T*>(a.a) + off, *pb = static_cast<const T*>(a.b) + off,
+          *pc = static_cast<const T*>(a.c) + off;
+  for (int i = tid; i < kSeg; i += 128) pw[i] = decay_pow(ld, i);
+  for (int i = tid; i < TQ * D / 4; i += 128) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);   // rows behind the end: zero, and so is their output
+    if (i0 + r < end) f = load4<T>(pa + (i0 + r) * stride + c);
+    *reinterpret_cast<float4*>(as + r * LDA + c) = f;
+  }
+  const int r0 = warp * 16 + g;   // this thread's rows: r0 and r0 + 8
+  float acc[NT][4] = {};
+  // the state's part: 32 rows of X at a time; the k index of a product is permuted (2t, 2t+1 for t, t+4)
+  const bool first = a.reverse ? seg == a.n_seg - 1 : seg == 0;
+  const float* X = a.n_seg == 1 ? a.initial : a.states;
+  if (X && i0 < end && !(first && !a.initial)) {
+    X += a.n_seg == 1 ? ((int64_t)b * a.H + h) * D * D : (((int64_t)b * a.H + h) * a.n_seg + seg) * D * D;
+    const float w0 = decay_pow(ld, a.reverse ? max((int64_t)0, end - 1 - (i0 + r0)) : i0 + r0 - s0 + 1);
+    const float w1 = decay_pow(ld, a.reverse ? max((int64_t)0, end - 1 - (i0 + r0 + 8)) : i0 + r0 + 8 - s0 + 1);
+    for (int k0 = 0; k0 < D; k0 += TK) {
+      __syncthreads();
+      if (!a.transposed) {
+        for (int i = tid; i < TK * D / 4; i += 128) {
+          const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+          *reinterpret_cast<float4*>(cs + r * LDC + c) = *reinterpret_cast<const float4*>(X + (k0 + r) * D + c);
+        }
+      } else {
+        for (int i = tid; i < TK * D; i += 128) cs[(i % TK) * LDC + i / TK] = X[(i / TK) * D + k0 + i % TK];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k8 = 0; k8 < TK / 8; ++k8) {
+        const float2 u = *reinterpret_cast<const float2*>(as + r0 * LDA + k0 + k8 * 8 + 2 * t);
+        const float2 v = *reinterpret_cast<const float2*>(as + (r0 + 8) * LDA + k0 + k8 * 8 + 2 * t);
+        const float av[4] = {u.x * w0, v.x * w1, u.y * w0, v.y * w1};
+        uint32_t ah[4], al[4];
+        a_terms<true>(av, ah, al);
+        const float* cr = cs + (k8 * 8 + 2 * t) * LDC + g;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_terms<true, true>(acc[n], ah, al, cr[n * 8], cr[LDC + n * 8]);
+      }
+    }
+  }
+  const int64_t jb = a.reverse ? i0 : s0, je = a.reverse ? end : min(end, i0 + TQ);
+  for (int64_t j0 = jb; j0 < je; j0 += TK) {
+    __syncthreads();
+    for (int i = tid; i < TK * D / 4; i += 128) {
+      const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+      float4 fb = make_float4(0.f, 0.f, 0.f, 0.f), fc = fb;
+      if (j0 + r < end) {
+        fb = load4<T>(pb + (j0 + r) * stride + c);
+        fc = load4<T>(pc + (j0 + r) * stride + c);
+      }
+      *reinterpret_cast<float4*>(bs + r * LDA + c) = fb;
+      *reinterpret_cast<float4*>(cs + r * LDC + c) = fc;
+    }
+    __syncthreads();
+    float p[TK / 8][4] = {};
+#pragma unroll 4
+    for (int k8 = 0; k8 < D / 8; ++k8) {
+      const float2 u = *reinterpret_cast<const float2*>(as + r0 * LDA + k8 * 8 + 2 * t);
+      const float2 v = *reinterpret_cast<const float2*>(as + (r0 + 8) * LDA + k8 * 8 + 2 * t);
+      const float av[4] = {u.x, v.x, u.y, v.y};
+      uint32_t ah[4], al[4];
+      a_terms<kF32>(av, ah, al);
+#pragma unroll
+      for (int n = 0; n < TK / 8; ++n) {
+        const float2 w = *reinterpret_cast<const float2*>(bs + (n * 8 + g) * LDA + k8 * 8 + 2 * t);
+        mma_terms<kF32, kF32>(p[n], ah, al, w.x, w.y);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < TK / 8; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int dist0 = (int)(i0 - j0) + r0 + (e / 2) * 8 - n * 8 - 2 * t - (e & 1);
+        const int dist = a.reverse ? -dist0 : dist0;
+        p[n][e] = dist < 0 ? 0.f : p[n][e] * pw[dist];
+      }
+      const float av[4] = {p[n][0], p[n][2], p[n][1], p[n][3]};
+      uint32_t ah[4], al[4];
+      a_terms<true>(av, ah, al);
+      const float* cr = cs + (n * 8 + 2 * t) * LDC + g;
+#pragma unroll
+      for (int m = 0; m < NT; ++m) mma_terms<true, kF32>(acc[m], ah, al, cr[m * 8], cr[LDC + m * 8]);
+    }
+  }
+  T* out = static_cast<T*>(a.out) + off;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int64_t i = i0 + r0 + half * 8;
+    if (i >= a.N) continue;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) store2(out + i * stride + n * 8 + 2 * t, acc[n][2 * half], acc[n][2 * half + 1]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// one token: state out = lam state in + k v^T, o = (state out)^T q
+// Bound by the state's 8 D^2 bytes per (item, head).  Columns of the state are independent: a CTA takes 32 of
+// them, 8 lanes x 16 bytes per row, and has all its loads in flight before the first product.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(256) lin_step_kernel(LinStepArgs a) {
+  constexpr int R = D / 32;   // rows per thread
+  __shared__ float4 part[8][8];
+  const int tid = threadIdx.x, cx = tid % 8, ry = tid / 8;
+  const int64_t bh = (int64_t)blockIdx.z * a.H + blockIdx.y;
+  const int col = blockIdx.x * 32 + cx * 4;
+  const float* in = a.state_in + bh * D * D + col;
+  float* out = a.state_out + bh * D * D + col;
+  float4 S[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) S[i] = *reinterpret_cast<const float4*>(in + (ry + 32 * i) * D);
+  const float lam = decay_pow(a.log_decay[blockIdx.y], 1);
+  const float4 v = load4<T>(static_cast<const T*>(a.v) + bh * D + col);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int r = ry + 32 * i;
+    const float k = to_f32(static_cast<const T*>(a.k)[bh * D + r]), q = to_f32(static_cast<const T*>(a.q)[bh * D + r]);
+    S[i].x = fmaf(k, v.x, lam * S[i].x);
+    S[i].y = fmaf(k, v.y, lam * S[i].y);
+    S[i].z = fmaf(k, v.z, lam * S[i].z);
+    S[i].w = fmaf(k, v.w, lam * S[i].w);
+    *reinterpret_cast<float4*>(out + r * D) = S[i];
+    o.x = fmaf(q, S[i].x, o.x);
+    o.y = fmaf(q, S[i].y, o.y);
+    o.z = fmaf(q, S[i].z, o.z);
+    o.w = fmaf(q, S[i].w, o.w);
+  }
+#pragma unroll
+  for (int m = 8; m < 32; m *= 2) {   // the four rows of a warp
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
+  }
+  if (tid % 32 < 8) part[tid / 32][cx] = o;
+  __syncthreads();
+  if (tid >= 8) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) {
+    const float4 x = part[w][cx];
+    o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+  }
+  T* y = static_cast<T*>(a.o) + bh * D + col;
+  store2(y, o.x, o.y);
+  store2(y + 2, o.z, o.w);
+}
+
+template <typename T, int D>
+cudaError_t map(const LinMapArgs& m, const Dims& d, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(lin_map_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       MapSmem<D>::bytes);
+  if (e != cudaSuccess) return e;
+  lin_map_kernel<T, D><<<dim3((unsigned)((d.N + TQ - 1) / TQ), d.H, d.B), 128, MapSmem<D>::bytes, s>>>(m);
+  return cudaGetLastError();
+}
+
+// Calls f with a value of the problem's element type and its head dim as a constant.
+template <typename F> cudaError_t dispatch(const Dims& d, kda_dtype dt, F f) {
+  using std::integral_constant;
+  if (dt == KDA_DT_BF16)
+    return d.dk == 128 ? f(__nv_bfloat16(), integral_constant<int, 128>()) : f(__nv_bfloat16(), integral_constant<int, 64>());
+  return d.dk == 128 ? f(float(), integral_constant<int, 128>()) : f(float(), integral_constant<int, 64>());
+}
+
+cudaError_t launch_local(const Dims& d, kda_dtype dt, const LinLocalArgs& a, cudaStream_t s) {
+  return dispatch(d, dt, [&](auto t, auto D) {
+    lin_local_kernel<decltype(t), decltype(D)::value><<<dim3((unsigned)a.n_seg, d.H, d.B), 256, 0, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+cudaError_t launch_scan(const Dims& d, const LinScanArgs& a, cudaStream_t s) {
+  lin_scan_kernel<<<dim3((unsigned)(a.dd / 512), d.B * d.H), 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+cudaError_t launch_map(const Dims& d, kda_dtype dt, const LinMapArgs& a, cudaStream_t s) {
+  return dispatch(d, dt, [&](auto t, auto D) { return map<decltype(t), decltype(D)::value>(a, d, s); });
+}
+
+int64_t segments(const Dims& d) { return (d.N + kSeg - 1) / kSeg; }
+size_t state_bytes(const Dims& d) { return (size_t)d.B * d.H * segments(d) * d.dk * d.dv * sizeof(float); }
+
+}  // namespace
+
+size_t linear_fwd_scratch(const Dims& d) { return state_bytes(d); }
+size_t linear_bwd_scratch(const Dims& d) { return 2 * state_bytes(d); }
+
+cudaError_t launch_linear_fwd(const Dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
+                              const float* log_decay, const int32_t* lengths, const float* S0, void* o, float* SN,
+                              void* scratch, cudaStream_t s, int* launches) {
+  cudaError_t e;
+  const int n_seg = (int)segments(d);
+  float* states = static_cast<float*>(scratch);
+  if (n_seg > 1 || SN) {
+    if (n_seg > 0) {
+      if ((e = launch_local(d, dt, {k, v, log_decay, lengths, states, d.N, d.H, n_seg, false}, s)) != cudaSuccess) return e;
+      *launches += 1;
+    }
+    if ((e = launch_scan(d, {states, S0, SN, log_decay, lengths, d.N, (int64_t)d.dk * d.dv, kSeg, d.H, n_seg, false}, s)) !=
+        cudaSuccess)
+      return e;
+    *launches += 1;
+  }
+  if (n_seg == 0) return cudaSuccess;
+  if ((e = launch_map(d, dt, {q, k, v, o, states, S0, log_decay, lengths, d.N, d.H, n_seg, false, false}, s)) != cudaSuccess)
+    return e;
+  *launches += 1;
+  return cudaSuccess;
+}
+
+cudaError_t launch_linear_bwd(const Dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
+                              const float* log_decay, const int32_t* lengths, const float* S0, const void* d_o,
+                              const float* dSN, void* dq, void* dk, void* dv, float* dS0, void* scratch,
+                              cudaStream_t s, int* launches) {
+  cudaError_t e;
+  const int n_seg = (int)segments(d);
+  const int64_t dd = (int64_t)d.dk * d.dv;
+  float* states = static_cast<float*>(scratch);
+  float* grads = states + state_bytes(d) / sizeof(float);
+  if (n_seg > 1) {
+    if ((e = launch_local(d, dt, {k, v, log_decay, lengths, states, d.N, d.H, n_seg, false}, s)) != cudaSuccess) return e;
+    if ((e = launch_scan(d, {states, S0, nullptr, log_decay, lengths, d.N, dd, kSeg, d.H, n_seg, false}, s)) != cudaSuccess)
+      return e;
+    *launches += 2;
+  }
+  if (n_seg > 1 || dS0) {
+    if (n_seg > 0) {
+      if ((e = launch_local(d, dt, {q, d_o, log_decay, lengths, grads, d.N, d.H, n_seg, true}, s)) != cudaSuccess) return e;
+      *launches += 1;
+    }
+    if ((e = launch_scan(d, {grads, dSN, dS0, log_decay, lengths, d.N, dd, kSeg, d.H, n_seg, true}, s)) != cudaSuccess)
+      return e;
+    *launches += 1;
+  }
+  if (n_seg == 0) return cudaSuccess;
+  if ((e = launch_map(d, dt, {d_o, v, k, dq, states, S0, log_decay, lengths, d.N, d.H, n_seg, false, true}, s)) !=
+          cudaSuccess ||
+      (e = launch_map(d, dt, {v, d_o, q, dk, grads, dSN, log_decay, lengths, d.N, d.H, n_seg, true, true}, s)) !=
+          cudaSuccess ||
+      (e = launch_map(d, dt, {k, q, d_o, dv, grads, dSN, log_decay, lengths, d.N, d.H, n_seg, true, false}, s)) !=
+          cudaSuccess)
+    return e;
+  *launches += 3;
+  return cudaSuccess;
+}
+
+cudaError_t launch_linear_step(const Dims& d, kda_dtype dt, const LinStepArgs& a, cudaStream_t s, int* launches) {
+  const cudaError_t e = dispatch(d, dt, [&](auto t, auto D) {
+    lin_step_kernel<decltype(t), decltype(D)::value><<<dim3(d.dv / 32, d.H, d.B), 256, 0, s>>>(a);
+    return cudaGetLastError();
+  });
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+}  // namespace kda
