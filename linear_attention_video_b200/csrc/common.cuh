@@ -146,15 +146,20 @@ struct LinStepArgs {
   float* state_out;
   int H;
 };
-size_t linear_fwd_scratch(const Dims& d);
-size_t linear_bwd_scratch(const Dims& d);
+size_t linear_fwd_scratch(const Dims& d, kda_dtype dt);
+size_t linear_bwd_scratch(const Dims& d, kda_dtype dt);
 cudaError_t launch_linear_fwd(const Dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
                               const float* log_decay, const int32_t* lengths, const float* S0, void* o, float* SN,
-                              void* scratch, cudaStream_t s, int* launches);
+                              void* scratch, uint32_t* status, cudaStream_t s, int* launches);
 cudaError_t launch_linear_bwd(const Dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
                               const float* log_decay, const int32_t* lengths, const float* S0, const void* d_o,
                               const float* dSN, void* dq, void* dk, void* dv, float* dS0, void* scratch,
-                              cudaStream_t s, int* launches);
+                              uint32_t* status, cudaStream_t s, int* launches);
+// bf16 problems (linear_tc.cu); the states between the launches are hi and lo images (see there).
+int linear_tc_segment();
+cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s);
+cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanArgs& a, bool local, cudaStream_t s);
+cudaError_t launch_linear_tc_map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s);
 cudaError_t launch_linear_step(const Dims& d, kda_dtype dt, const LinStepArgs& a, cudaStream_t s, int* launches);
 
 // Host-side validation (kda_api.cu), returning a kda_status.

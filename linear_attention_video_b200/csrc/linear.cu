@@ -12,8 +12,8 @@
 // Three launches: every segment's own contribution sum_t w_t x_t y_t^T to the state behind it (before it, for
 // G); the recurrence over segments, element by element; the map, whose tiles are then independent.
 //
-// The matrix products here run on mma.sync in tf32 with each fp32 operand split into two terms (three products,
-// 2^-22 relative), so fp32 problems keep fp32 accuracy; bf16 inputs are exact in tf32 and need one term.
+// bf16 problems run these launches on tcgen05 (linear_tc.cu).  The matrix products here, of fp32 problems, run on
+// mma.sync in tf32 with each operand split into two terms (three products, 2^-22 relative): fp32 accuracy.
 // Decays are lam^n = exp(n log lam) of whole n >= 0: never above 1, so nothing overflows however fast a head
 // forgets, and the fp32 error of n log lam, 2^-25 |n log lam|, is largest beside e^-1.
 #include <algorithm>
@@ -52,34 +52,22 @@ __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], cons
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// d += A B with A and B in one (exact) or two (split) terms each.
-template <bool SplitA, bool SplitB>
-__device__ __forceinline__ void mma_terms(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float b0,
-                                          float b1) {
+// d += A B, both operands in two terms (lo lo, 2^-22 of the product, is left out).
+__device__ __forceinline__ void mma3(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float b0, float b1) {
   uint32_t bh[2], bl[2];
-  if constexpr (SplitB) {
-    split(b0, bh[0], bl[0]);
-    split(b1, bh[1], bl[1]);
-    mma8(d, ah, bl);
-  } else {
-    bh[0] = __float_as_uint(b0);
-    bh[1] = __float_as_uint(b1);
-  }
-  if constexpr (SplitA) mma8(d, al, bh);
+  split(b0, bh[0], bl[0]);
+  split(b1, bh[1], bl[1]);
+  mma8(d, ah, bl);
+  mma8(d, al, bh);
   mma8(d, ah, bh);
 }
-template <bool Split>
-__device__ __forceinline__ void a_terms(const float (&x)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+__device__ __forceinline__ void split4(const float (&x)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (Split) split(x[i], hi[i], lo[i]);
-    else hi[i] = __float_as_uint(x[i]), lo[i] = 0u;
-  }
+  for (int i = 0; i < 4; ++i) split(x[i], hi[i], lo[i]);
 }
 
-template <typename T> __device__ __forceinline__ float4 load4(const T* p);
-template <> __device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
   const uint2 u = *reinterpret_cast<const uint2*>(p);
   const float2 a = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(&u)[0]);
   const float2 b = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(&u)[1]);
@@ -98,19 +86,18 @@ constexpr int kSeg = 256;    // tokens per segment
 // a segment's own contribution: local[x][y] = sum_t w_t x_t y_t^T
 // w_t = lam^(s0+n-1-t) (state behind it), or lam^(t-s0+1) (gradient before it)
 // ---------------------------------------------------------------------------
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) lin_local_kernel(LinLocalArgs a) {
   constexpr int LD = D + 8;            // rows 8 banks apart: A and B fragments without conflicts
   constexpr int RG = D / 16, CG = 8 / RG, NT = D / CG / 8;
-  constexpr bool kF32 = sizeof(T) == 4;
   __shared__ float xs[TK * LD], ys[TK * LD];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int64_t s0 = (int64_t)seg * kSeg, end = min(item_tokens(a.lengths, b, a.N), s0 + kSeg);
   const float ld = a.log_decay[h];
   const int64_t stride = (int64_t)a.H * D;
-  const T* x = static_cast<const T*>(a.x) + (int64_t)b * a.N * stride + (int64_t)h * D;
-  const T* y = static_cast<const T*>(a.y) + (int64_t)b * a.N * stride + (int64_t)h * D;
+  const float* x = static_cast<const float*>(a.x) + (int64_t)b * a.N * stride + (int64_t)h * D;
+  const float* y = static_cast<const float*>(a.y) + (int64_t)b * a.N * stride + (int64_t)h * D;
   const int m0 = (warp % RG) * 16, n0 = (warp / RG) * (D / CG);
   float acc[NT][4] = {};
   for (int64_t t0 = s0; t0 < end; t0 += TK) {
@@ -119,8 +106,8 @@ __global__ void __launch_bounds__(256) lin_local_kernel(LinLocalArgs a) {
       const int r = i / (D / 4), c = (i % (D / 4)) * 4;
       float4 fx = make_float4(0.f, 0.f, 0.f, 0.f), fy = fx;
       if (t0 + r < end) {
-        fx = load4<T>(x + (t0 + r) * stride + c);
-        fy = load4<T>(y + (t0 + r) * stride + c);
+        fx = load4(x + (t0 + r) * stride + c);
+        fy = load4(y + (t0 + r) * stride + c);
         const float w = decay_pow(ld, a.reverse ? t0 + r - s0 + 1 : end - 1 - t0 - r);
         fy.x *= w; fy.y *= w; fy.z *= w; fy.w *= w;
       }
@@ -133,11 +120,11 @@ __global__ void __launch_bounds__(256) lin_local_kernel(LinLocalArgs a) {
       const float* xr = xs + (k8 * 8 + t) * LD + m0 + g;
       const float av[4] = {xr[0], xr[8], xr[4 * LD], xr[4 * LD + 8]};
       uint32_t ah[4], al[4];
-      a_terms<kF32>(av, ah, al);
+      split4(av, ah, al);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float* yr = ys + (k8 * 8 + t) * LD + n0 + n * 8 + g;
-        mma_terms<kF32, true>(acc[n], ah, al, yr[0], yr[4 * LD]);
+        mma3(acc[n], ah, al, yr[0], yr[4 * LD]);
       }
     }
   }
@@ -204,11 +191,10 @@ template <int D> struct MapSmem {
   static constexpr int bytes = floats * (int)sizeof(float);
 };
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128) lin_map_kernel(LinMapArgs a) {
   using L = MapSmem<D>;
   constexpr int LDA = L::LDA, LDC = L::LDC, NT = D / 8;
-  constexpr bool kF32 = sizeof(T) == 4;
   extern __shared__ float sm[];
   float* as = sm;
   float* bs = as + TQ * LDA;
@@ -221,13 +207,13 @@ __global__ void __launch_bounds__(128) lin_map_kernel(LinMapArgs a) {
   const int64_t s0 = (int64_t)seg * kSeg, len = item_tokens(a.lengths, b, a.N), end = min(len, s0 + kSeg);
   const float ld = a.log_decay[h];
   const int64_t stride = (int64_t)a.H * D, off = (int64_t)b * a.N * stride + (int64_t)h * D;
-  const T *pa = static_cast<const T*>(a.a) + off, *pb = static_cast<const T*>(a.b) + off,
-          *pc = static_cast<const T*>(a.c) + off;
+  const float *pa = static_cast<const float*>(a.a) + off, *pb = static_cast<const float*>(a.b) + off,
+              *pc = static_cast<const float*>(a.c) + off;
   for (int i = tid; i < kSeg; i += 128) pw[i] = decay_pow(ld, i);
   for (int i = tid; i < TQ * D / 4; i += 128) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);   // rows behind the end: zero, and so is their output
-    if (i0 + r < end) f = load4<T>(pa + (i0 + r) * stride + c);
+    if (i0 + r < end) f = load4(pa + (i0 + r) * stride + c);
     *reinterpret_cast<float4*>(as + r * LDA + c) = f;
   }
   const int r0 = warp * 16 + g;   // this thread's rows: r0 and r0 + 8
@@ -256,10 +242,10 @@ __global__ void __launch_bounds__(128) lin_map_kernel(LinMapArgs a) {
         const float2 v = *reinterpret_cast<const float2*>(as + (r0 + 8) * LDA + k0 + k8 * 8 + 2 * t);
         const float av[4] = {u.x * w0, v.x * w1, u.y * w0, v.y * w1};
         uint32_t ah[4], al[4];
-        a_terms<true>(av, ah, al);
+        split4(av, ah, al);
         const float* cr = cs + (k8 * 8 + 2 * t) * LDC + g;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_terms<true, true>(acc[n], ah, al, cr[n * 8], cr[LDC + n * 8]);
+        for (int n = 0; n < NT; ++n) mma3(acc[n], ah, al, cr[n * 8], cr[LDC + n * 8]);
       }
     }
   }
@@ -270,8 +256,8 @@ __global__ void __launch_bounds__(128) lin_map_kernel(LinMapArgs a) {
       const int r = i / (D / 4), c = (i % (D / 4)) * 4;
       float4 fb = make_float4(0.f, 0.f, 0.f, 0.f), fc = fb;
       if (j0 + r < end) {
-        fb = load4<T>(pb + (j0 + r) * stride + c);
-        fc = load4<T>(pc + (j0 + r) * stride + c);
+        fb = load4(pb + (j0 + r) * stride + c);
+        fc = load4(pc + (j0 + r) * stride + c);
       }
       *reinterpret_cast<float4*>(bs + r * LDA + c) = fb;
       *reinterpret_cast<float4*>(cs + r * LDC + c) = fc;
@@ -284,11 +270,11 @@ __global__ void __launch_bounds__(128) lin_map_kernel(LinMapArgs a) {
       const float2 v = *reinterpret_cast<const float2*>(as + (r0 + 8) * LDA + k8 * 8 + 2 * t);
       const float av[4] = {u.x, v.x, u.y, v.y};
       uint32_t ah[4], al[4];
-      a_terms<kF32>(av, ah, al);
+      split4(av, ah, al);
 #pragma unroll
       for (int n = 0; n < TK / 8; ++n) {
         const float2 w = *reinterpret_cast<const float2*>(bs + (n * 8 + g) * LDA + k8 * 8 + 2 * t);
-        mma_terms<kF32, kF32>(p[n], ah, al, w.x, w.y);
+        mma3(p[n], ah, al, w.x, w.y);
       }
     }
 #pragma unroll
@@ -301,13 +287,13 @@ __global__ void __launch_bounds__(128) lin_map_kernel(LinMapArgs a) {
       }
       const float av[4] = {p[n][0], p[n][2], p[n][1], p[n][3]};
       uint32_t ah[4], al[4];
-      a_terms<true>(av, ah, al);
+      split4(av, ah, al);
       const float* cr = cs + (n * 8 + 2 * t) * LDC + g;
 #pragma unroll
-      for (int m = 0; m < NT; ++m) mma_terms<true, kF32>(acc[m], ah, al, cr[m * 8], cr[LDC + m * 8]);
+      for (int m = 0; m < NT; ++m) mma3(acc[m], ah, al, cr[m * 8], cr[LDC + m * 8]);
     }
   }
-  T* out = static_cast<T*>(a.out) + off;
+  float* out = static_cast<float*>(a.out) + off;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int64_t i = i0 + r0 + half * 8;
@@ -335,7 +321,7 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepArgs a) {
 #pragma unroll
   for (int i = 0; i < R; ++i) S[i] = *reinterpret_cast<const float4*>(in + (ry + 32 * i) * D);
   const float lam = decay_pow(a.log_decay[blockIdx.y], 1);
-  const float4 v = load4<T>(static_cast<const T*>(a.v) + bh * D + col);
+  const float4 v = load4(static_cast<const T*>(a.v) + bh * D + col);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -371,12 +357,12 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepArgs a) {
   store2(y + 2, o.z, o.w);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t map(const LinMapArgs& m, const Dims& d, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(lin_map_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(lin_map_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        MapSmem<D>::bytes);
   if (e != cudaSuccess) return e;
-  lin_map_kernel<T, D><<<dim3((unsigned)((d.N + TQ - 1) / TQ), d.H, d.B), 128, MapSmem<D>::bytes, s>>>(m);
+  lin_map_kernel<D><<<dim3((unsigned)((d.N + TQ - 1) / TQ), d.H, d.B), 128, MapSmem<D>::bytes, s>>>(m);
   return cudaGetLastError();
 }
 
@@ -388,85 +374,95 @@ template <typename F> cudaError_t dispatch(const Dims& d, kda_dtype dt, F f) {
   return d.dk == 128 ? f(float(), integral_constant<int, 128>()) : f(float(), integral_constant<int, 64>());
 }
 
-cudaError_t launch_local(const Dims& d, kda_dtype dt, const LinLocalArgs& a, cudaStream_t s) {
-  return dispatch(d, dt, [&](auto t, auto D) {
-    lin_local_kernel<decltype(t), decltype(D)::value><<<dim3((unsigned)a.n_seg, d.H, d.B), 256, 0, s>>>(a);
-    return cudaGetLastError();
-  });
+cudaError_t launch_local(const Dims& d, const LinLocalArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)a.n_seg, d.H, d.B);
+  if (d.dk == 128) lin_local_kernel<128><<<grid, 256, 0, s>>>(a);
+  else lin_local_kernel<64><<<grid, 256, 0, s>>>(a);
+  return cudaGetLastError();
 }
 cudaError_t launch_scan(const Dims& d, const LinScanArgs& a, cudaStream_t s) {
   lin_scan_kernel<<<dim3((unsigned)(a.dd / 512), d.B * d.H), 128, 0, s>>>(a);
   return cudaGetLastError();
 }
-cudaError_t launch_map(const Dims& d, kda_dtype dt, const LinMapArgs& a, cudaStream_t s) {
-  return dispatch(d, dt, [&](auto t, auto D) { return map<decltype(t), decltype(D)::value>(a, d, s); });
+cudaError_t launch_map(const Dims& d, const LinMapArgs& a, cudaStream_t s) {
+  return d.dk == 128 ? map<128>(a, d, s) : map<64>(a, d, s);
 }
 
-int64_t segments(const Dims& d) { return (d.N + kSeg - 1) / kSeg; }
-size_t state_bytes(const Dims& d) { return (size_t)d.B * d.H * segments(d) * d.dk * d.dv * sizeof(float); }
+// What a pass over one problem needs to know: its kernels' segment length, and the three launches.
+struct Pass {
+  const Dims& d;
+  bool tc;
+  int seg, n_seg;
+  const float* log_decay;
+  const int32_t* lengths;
+  uint32_t* status;
+  cudaStream_t s;
+  int* launches;
+
+  Pass(const Dims& d_, kda_dtype dt, const float* ld, const int32_t* len, uint32_t* st, cudaStream_t s_, int* l)
+      : d(d_), tc(dt == KDA_DT_BF16), seg(tc ? linear_tc_segment() : kSeg),
+        n_seg((int)((d_.N + seg - 1) / seg)), log_decay(ld), lengths(len), status(st), s(s_), launches(l) {}
+
+  size_t state_floats() const { return (size_t)d.B * d.H * n_seg * d.dk * d.dv; }
+
+  // What enters every segment (in the direction of the pass) of sum w x y^T; `last`: what leaves the last one.
+  cudaError_t states(const void* x, const void* y, float* out, const float* initial, float* last, bool reverse) {
+    const bool local = n_seg > 1 || (n_seg == 1 && last);
+    if (!local && !last && !(tc && initial)) return cudaSuccess;   // nothing enters, or the initial state as it is
+    cudaError_t e;
+    if (local) {
+      const LinLocalArgs a{x, y, log_decay, lengths, out, d.N, d.H, n_seg, reverse};
+      if ((e = tc ? launch_linear_tc_local(d, a, status, s) : launch_local(d, a, s)) != cudaSuccess) return e;
+      *launches += 1;
+    }
+    const LinScanArgs a{out, initial, last, log_decay, lengths, d.N, (int64_t)d.dk * d.dv, seg, d.H, n_seg, reverse};
+    if ((e = tc ? launch_linear_tc_scan(d, a, local, s) : launch_scan(d, a, s)) != cudaSuccess) return e;
+    *launches += 1;
+    return cudaSuccess;
+  }
+
+  cudaError_t map(const void* a, const void* b, const void* c, void* out, const float* st, const float* initial,
+                  bool reverse, bool transposed) {
+    if (n_seg == 0) return cudaSuccess;
+    const LinMapArgs m{a, b, c, out, st, initial, log_decay, lengths, d.N, d.H, n_seg, reverse, transposed};
+    const cudaError_t e = tc ? launch_linear_tc_map(d, m, status, s) : launch_map(d, m, s);
+    if (e == cudaSuccess) *launches += 1;
+    return e;
+  }
+};
+
+size_t state_bytes(const Dims& d, kda_dtype dt) {
+  return Pass(d, dt, nullptr, nullptr, nullptr, nullptr, nullptr).state_floats() * sizeof(float);
+}
 
 }  // namespace
 
-size_t linear_fwd_scratch(const Dims& d) { return state_bytes(d); }
-size_t linear_bwd_scratch(const Dims& d) { return 2 * state_bytes(d); }
+size_t linear_fwd_scratch(const Dims& d, kda_dtype dt) { return state_bytes(d, dt); }
+size_t linear_bwd_scratch(const Dims& d, kda_dtype dt) { return 2 * state_bytes(d, dt); }
 
 cudaError_t launch_linear_fwd(const Dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
                               const float* log_decay, const int32_t* lengths, const float* S0, void* o, float* SN,
-                              void* scratch, cudaStream_t s, int* launches) {
-  cudaError_t e;
-  const int n_seg = (int)segments(d);
+                              void* scratch, uint32_t* status, cudaStream_t s, int* launches) {
+  Pass p(d, dt, log_decay, lengths, status, s, launches);
   float* states = static_cast<float*>(scratch);
-  if (n_seg > 1 || SN) {
-    if (n_seg > 0) {
-      if ((e = launch_local(d, dt, {k, v, log_decay, lengths, states, d.N, d.H, n_seg, false}, s)) != cudaSuccess) return e;
-      *launches += 1;
-    }
-    if ((e = launch_scan(d, {states, S0, SN, log_decay, lengths, d.N, (int64_t)d.dk * d.dv, kSeg, d.H, n_seg, false}, s)) !=
-        cudaSuccess)
-      return e;
-    *launches += 1;
-  }
-  if (n_seg == 0) return cudaSuccess;
-  if ((e = launch_map(d, dt, {q, k, v, o, states, S0, log_decay, lengths, d.N, d.H, n_seg, false, false}, s)) != cudaSuccess)
-    return e;
-  *launches += 1;
-  return cudaSuccess;
+  cudaError_t e;
+  if ((e = p.states(k, v, states, S0, SN, false)) != cudaSuccess) return e;
+  return p.map(q, k, v, o, states, S0, false, false);
 }
 
 cudaError_t launch_linear_bwd(const Dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
                               const float* log_decay, const int32_t* lengths, const float* S0, const void* d_o,
                               const float* dSN, void* dq, void* dk, void* dv, float* dS0, void* scratch,
-                              cudaStream_t s, int* launches) {
-  cudaError_t e;
-  const int n_seg = (int)segments(d);
-  const int64_t dd = (int64_t)d.dk * d.dv;
+                              uint32_t* status, cudaStream_t s, int* launches) {
+  Pass p(d, dt, log_decay, lengths, status, s, launches);
   float* states = static_cast<float*>(scratch);
-  float* grads = states + state_bytes(d) / sizeof(float);
-  if (n_seg > 1) {
-    if ((e = launch_local(d, dt, {k, v, log_decay, lengths, states, d.N, d.H, n_seg, false}, s)) != cudaSuccess) return e;
-    if ((e = launch_scan(d, {states, S0, nullptr, log_decay, lengths, d.N, dd, kSeg, d.H, n_seg, false}, s)) != cudaSuccess)
-      return e;
-    *launches += 2;
-  }
-  if (n_seg > 1 || dS0) {
-    if (n_seg > 0) {
-      if ((e = launch_local(d, dt, {q, d_o, log_decay, lengths, grads, d.N, d.H, n_seg, true}, s)) != cudaSuccess) return e;
-      *launches += 1;
-    }
-    if ((e = launch_scan(d, {grads, dSN, dS0, log_decay, lengths, d.N, dd, kSeg, d.H, n_seg, true}, s)) != cudaSuccess)
-      return e;
-    *launches += 1;
-  }
-  if (n_seg == 0) return cudaSuccess;
-  if ((e = launch_map(d, dt, {d_o, v, k, dq, states, S0, log_decay, lengths, d.N, d.H, n_seg, false, true}, s)) !=
-          cudaSuccess ||
-      (e = launch_map(d, dt, {v, d_o, q, dk, grads, dSN, log_decay, lengths, d.N, d.H, n_seg, true, true}, s)) !=
-          cudaSuccess ||
-      (e = launch_map(d, dt, {k, q, d_o, dv, grads, dSN, log_decay, lengths, d.N, d.H, n_seg, true, false}, s)) !=
-          cudaSuccess)
-    return e;
-  *launches += 3;
-  return cudaSuccess;
+  float* grads = states + p.state_floats();
+  cudaError_t e;
+  if ((e = p.states(k, v, states, S0, nullptr, false)) != cudaSuccess) return e;
+  if ((e = p.states(q, d_o, grads, dSN, dS0, true)) != cudaSuccess) return e;
+  if ((e = p.map(d_o, v, k, dq, states, S0, false, true)) != cudaSuccess) return e;
+  if ((e = p.map(v, d_o, q, dk, grads, dSN, true, true)) != cudaSuccess) return e;
+  return p.map(k, q, d_o, dv, grads, dSN, true, false);
 }
 
 cudaError_t launch_linear_step(const Dims& d, kda_dtype dt, const LinStepArgs& a, cudaStream_t s, int* launches) {

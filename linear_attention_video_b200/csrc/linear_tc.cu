@@ -1,0 +1,613 @@
+// Linear attention with a fixed decay per head on the tensor cores (tcgen05), bf16 problems.
+//
+// The three launches of linear.cu, for bf16 inputs:
+//   local: each segment's own sum_t w_t x_t y_t^T, [D x tokens] x [tokens x D] products;
+//   scan:  the recurrence over segments, element by element in fp32;
+//   map:   out_i = lam^e(i) X^(T) a_i + sum_j lam^|i-j| (a_i . b_j) c_j, 128 rows per CTA.
+// The decay is a constant of the head, so no tile needs a running maximum or an exponential of its own: with a
+// column's place cc in its group of 32, lam^(i-j) = lam^(i - group's last) * lam^(31-cc), a factor per (row, group)
+// times one of 32 registers, both at most 1.  Only the 32 x 32 blocks on the diagonal look lam^(i-j) up.
+//
+// What is rounded: the decayed scores go to bf16 for their second product, as in any attention on these units
+// (2^-9 of each score at random, as much as the output's own rounding); a state enters a product as two bf16 terms
+// (16 bits), since the whole past of a slowly forgetting head passes through it; the sums that become a state are
+// taken of three bf16 terms (24 bits), because states are fp32 results.  All sums are fp32.
+//
+// State images.  Between scan and map a state is two bf16 matrices (hi, lo) in the 128-byte-swizzled panels that
+// the tensor core reads, so a CTA fetches each with one bulk copy.  A segment's local state lies in the same
+// places, four fp32 where eight bf16 of hi will be and four where those of lo will be, so the scan works in place.
+#include "common.cuh"
+#include "tc.cuh"
+#include "tmap.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kSeg = 512;     // tokens per segment
+constexpr int TM = 128;       // tokens per tile of the map
+constexpr int TL = 64;        // tokens per tile of the local sums
+
+__device__ __forceinline__ float decay_pow(float log_decay, int64_t n) {
+  return n == 0 ? 1.f : expf((float)n * log_decay);
+}
+__device__ __forceinline__ int64_t item_tokens(const int32_t* lengths, int b, int64_t N) {
+  if (!lengths) return N;
+  const int64_t n = lengths[b];
+  return n < 0 ? 0 : (n > N ? N : n);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(v);
+}
+// a, b = bf16 pair + the rest
+__device__ __forceinline__ uint32_t take2(float& a, float& b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  a -= __low2float(v);
+  b -= __high2float(v);
+  return reinterpret_cast<const uint32_t&>(v);
+}
+// Bounded wait; a wait that gives up sets the CTA's flag, and every later wait returns at once.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitNs) { *abort_flag = 1; return false; }
+  }
+  return true;
+}
+// The same for a whole warp: one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
+}
+
+// Byte offset of 16-byte chunk c8 of row r in an image of rows x (64 columns per panel).
+__device__ __forceinline__ uint32_t image_off(int rows, int r, int c8) {
+  return (uint32_t)((c8 >> 3) * rows * 128 + r * 128 + (((c8 ^ r) & 7) << 4));
+}
+
+// ---------------------------------------------------------------------------
+// local
+// ---------------------------------------------------------------------------
+// One CTA per (segment, 128 channels, item): one head of 128, or two of 64 side by side (a 64-channel head is a
+// panel of the operand, so the pair's products are the diagonal blocks of a 128 x 128 one).  Per 64-token tile eight
+// warps turn y into the three bf16 terms of w y, hi over y itself; D[x][y] += x^T hi goes to one accumulator, the
+// mid and lo terms to another, so the main one sees one addition per 16 tokens.  Two stages of x and y and the
+// mid and lo images are 96 KB: two CTAs per SM, one's products under the other's roundings.
+constexpr int kLocalThreads = 288;
+constexpr int kLocalSmem = 1024 + 2 * 32768 + 32768;
+
+struct LocalMaps { CUtensorMap x, y; };
+
+template <int D>
+__global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __grid_constant__ LocalMaps maps,
+                                                                       LinLocalArgs a, uint32_t* status) {
+  extern __shared__ uint8_t dyn[];
+  __shared__ uint64_t full[2], ready, done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_slot;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+  uint8_t* mid = sm + 65536;
+  uint8_t* lo = mid + 16384;
+  volatile int* abort_flag = &abort_slot;
+  const int tid = threadIdx.x, warp = tid / 32;
+  constexpr int HP = 128 / D;   // heads per CTA
+  const int seg = blockIdx.x, h0 = blockIdx.y * HP, b = blockIdx.z;
+  const int64_t s0 = (int64_t)seg * kSeg, len = item_tokens(a.lengths, b, a.N), end = min(len, s0 + kSeg);
+  const int n_tok = (int)max((int64_t)0, end - s0), n_tiles = (n_tok + TL - 1) / TL;
+  if (tid == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    mbar_init(&ready, 256);
+    mbar_init(&done, 1);
+    abort_slot = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) { tmem_alloc(&tmem_slot, 256); tmem_relinquish(); }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tm = tmem_slot;
+  bool ok = true;
+
+  if (warp == 8) {
+    if (tid == 256) {
+      auto load = [&](int t) {
+        uint8_t* x = sm + (t & 1) * 32768;
+        mbar_arrive_expect_tx(&full[t & 1], 32768);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int c = D == 128 ? 64 * p : 0, h = D == 128 ? h0 : h0 + p, tok = (int)(s0 + t * TL);
+          tma_load_4d(x + p * 8192, &maps.x, c, h, tok, b, &full[t & 1]);
+          tma_load_4d(x + 16384 + p * 8192, &maps.y, c, h, tok, b, &full[t & 1]);
+        }
+      };
+      constexpr uint32_t id = idesc_bf16(128, 128, true, true);
+      int loaded = 0;
+      while (loaded < min(2, n_tiles)) load(loaded++);
+      for (int t = 0; ok && t < n_tiles; ++t) {
+        ok = wait_or_abort(&ready, t & 1, abort_flag);
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t xs = smem_u32(sm + (t & 1) * 32768);
+        const uint64_t dx = mdesc0(xs, 8192), dh = mdesc0(xs + 16384, 8192), dm = mdesc0(smem_u32(mid), 8192),
+                       dl = mdesc0(smem_u32(lo), 8192);
+#pragma unroll
+        for (int k = 0; k < TL / 16; ++k) {
+          mma_ss(tm, dx + mstep(k), dh + mstep(k), id, t || k);
+          mma_ss(tm + 128, dx + mstep(k), dl + mstep(k), id, t || k);
+          mma_ss(tm + 128, dx + mstep(k), dm + mstep(k), id, 1u);
+        }
+        mma_commit(&done);
+        if (loaded < n_tiles) {
+          ok = wait_or_abort(&done, t & 1, abort_flag);
+          if (ok) load(loaded++);
+        }
+      }
+      if (!ok)   // copies in flight end before the CTA does
+        for (int t = max(0, loaded - 2); t < loaded; ++t) mbar_wait(&full[t & 1], (t >> 1) & 1, 100000000ull);
+    }
+    __syncwarp();
+  } else {
+    const int c8 = tid % 16, r0 = tid / 16;   // this thread's 8 channels, its tokens r0 + 16 i
+    const int h = D == 128 ? h0 : min(h0 + c8 / 8, a.H - 1);
+    const float ld = a.log_decay[h];
+    for (int t = 0; ok && t < n_tiles; ++t) {
+      ok = warp_wait(&full[t & 1], (t >> 1) & 1, abort_flag);
+      if (ok && t > 0) ok = warp_wait(&done, (t - 1) & 1, abort_flag);   // mid and lo free
+      if (!ok) break;
+      uint8_t* x = sm + (t & 1) * 32768;
+      uint8_t* y = x + 16384;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 16 * i, tok = t * TL + r;
+        const uint32_t off = image_off(TL, r, c8);
+        uint4 hi, m, l;
+        if (tok < n_tok) {
+          const float w = decay_pow(ld, a.reverse ? tok + 1 : n_tok - 1 - tok);
+          const uint4 u = *reinterpret_cast<const uint4*>(y + off);
+          const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&u);
+          uint32_t *ph = &hi.x, *pm = &m.x, *pl = &l.x;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float2 f = __bfloat1622float2(e[j]);
+            f.x *= w;
+            f.y *= w;
+            ph[j] = take2(f.x, f.y);
+            pm[j] = take2(f.x, f.y);
+            pl[j] = pack2(f.x, f.y);
+          }
+        } else {   // behind the end, whatever stands there
+          hi = m = l = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(x + off) = hi;
+        }
+        *reinterpret_cast<uint4*>(y + off) = hi;
+        *reinterpret_cast<uint4*>(mid + off) = m;
+        *reinterpret_cast<uint4*>(lo + off) = l;
+      }
+      fence_proxy_async();
+      mbar_arrive(&ready);
+    }
+    if (ok && n_tiles) ok = warp_wait(&done, (n_tiles - 1) & 1, abort_flag);
+    if (ok) {
+      fence_after_sync();
+      // lane = row of the 128 x 128 block; head = row / D owns columns of the same block
+      const int row = (warp & 3) * 32 + (tid & 31), hp = row / D, r = row % D;
+      constexpr int COLS = D / 2;   // columns of this warp: a half of its head's
+      const int c0 = hp * D % 128 + (warp >> 2) * COLS;
+      const bool live = h0 + hp < a.H;
+      uint8_t* img = reinterpret_cast<uint8_t*>(a.local) + ((((int64_t)b * a.H + h0 + hp) * a.n_seg + seg) * D * D) * 4;
+#pragma unroll
+      for (int c = 0; c < COLS; c += 16) {
+        float v[16], w[16];
+        if (n_tiles) {
+          tmem_ld16(tm + ((uint32_t)((warp & 3) * 32) << 16) + c0 + c, v);
+          tmem_ld16(tm + ((uint32_t)((warp & 3) * 32) << 16) + 128 + c0 + c, w);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = w[i] = 0.f;
+        }
+        if (live) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 8) {
+            const uint32_t off = image_off(D, r, (c0 - hp * D % 128 + c + i) / 8);
+            *reinterpret_cast<float4*>(img + off) = make_float4(v[i] + w[i], v[i + 1] + w[i + 1], v[i + 2] + w[i + 2], v[i + 3] + w[i + 3]);
+            *reinterpret_cast<float4*>(img + D * D * 2 + off) =
+                make_float4(v[i + 4] + w[i + 4], v[i + 5] + w[i + 5], v[i + 6] + w[i + 6], v[i + 7] + w[i + 7]);
+          }
+        }
+      }
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (tid == 0 && *abort_flag) set_status(status, KDA_ERR_TIMEOUT);
+  fence_after_sync();
+  if (warp == 8) tmem_dealloc(tm, 256);
+}
+
+// ---------------------------------------------------------------------------
+// scan
+// ---------------------------------------------------------------------------
+// The decay of a whole segment multiplies a state again and again, so its fp32 rounding would add up; it is kept
+// in two fp32 terms of the fp64 power.
+struct Factor { float hi, lo; };
+__device__ __forceinline__ Factor segment_factor(float log_decay, int64_t n) {
+  const double f = n == 0 ? 1.0 : exp((double)n * (double)log_decay);
+  const float hi = (float)f;
+  return {hi, (float)(f - (double)hi)};
+}
+
+// A thread takes 8 columns of one row: 32 bytes of the local state, 16 each of the hi and lo images over them.
+// local = false: nothing but the initial state enters (one segment, no final state wanted).
+template <int D>
+__global__ void __launch_bounds__(128) lin_tc_scan_kernel(LinScanArgs a, bool local) {
+  const int bh = blockIdx.y, h = bh % a.H, b = bh / a.H;
+  const int e = blockIdx.x * 128 + threadIdx.x, r = e / (D / 8), c8 = e % (D / 8);
+  const int64_t len = item_tokens(a.lengths, b, a.N), last = len / a.seg;
+  const float ld = a.log_decay[h];
+  const Factor whole = segment_factor(ld, a.seg), part = segment_factor(ld, len % a.seg);
+  float S[8] = {};
+  if (a.initial) {
+    const float4* p = reinterpret_cast<const float4*>(a.initial + (int64_t)bh * D * D + r * D + c8 * 8);
+    const float4 u = p[0], v = p[1];
+    S[0] = u.x; S[1] = u.y; S[2] = u.z; S[3] = u.w; S[4] = v.x; S[5] = v.y; S[6] = v.z; S[7] = v.w;
+  }
+  uint8_t* p = reinterpret_cast<uint8_t*>(a.states + (int64_t)bh * a.n_seg * D * D) + image_off(D, r, c8);
+  constexpr int U = 4, LO = D * D * 2;
+  for (int c0 = 0; c0 < a.n_seg; c0 += U) {
+    float4 x[U], y[U];
+    if (local) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + u < a.n_seg) {
+          const uint8_t* s = p + (int64_t)(a.reverse ? a.n_seg - 1 - c0 - u : c0 + u) * D * D * 4;
+          x[u] = *reinterpret_cast<const float4*>(s);
+          y[u] = *reinterpret_cast<const float4*>(s + LO);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c0 + u >= a.n_seg) break;
+      const int c = a.reverse ? a.n_seg - 1 - c0 - u : c0 + u;
+      uint8_t* s = p + (int64_t)c * D * D * 4;
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = S[i];
+      uint4 hi, lo;
+      hi.x = take2(t[0], t[1]); hi.y = take2(t[2], t[3]); hi.z = take2(t[4], t[5]); hi.w = take2(t[6], t[7]);
+      lo.x = pack2(t[0], t[1]); lo.y = pack2(t[2], t[3]); lo.z = pack2(t[4], t[5]); lo.w = pack2(t[6], t[7]);
+      *reinterpret_cast<uint4*>(s) = hi;
+      *reinterpret_cast<uint4*>(s + LO) = lo;
+      if (c > last || !local) continue;   // behind the end: no tokens
+      const Factor f = c == last ? part : whole;
+      const float l[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) S[i] = fmaf(f.hi, S[i], fmaf(f.lo, S[i], l[i]));
+    }
+  }
+  if (a.final) {
+    float4* q = reinterpret_cast<float4*>(a.final + (int64_t)bh * D * D + r * D + c8 * 8);
+    q[0] = make_float4(S[0], S[1], S[2], S[3]);
+    q[1] = make_float4(S[4], S[5], S[6], S[7]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// map
+// ---------------------------------------------------------------------------
+// One CTA per 128 output rows: warps 0-3 hold a row per thread, one thread of warp 4 issues copies and products.
+//   O = a (Xhi + Xlo), scaled row by row by lam^e(i); then per tile of 128 tokens S = a b^T, P = bf16(S * decay)
+//   written over S in tensor memory, O += P c.
+// S and O take 256 columns of tensor memory and a, b, c 96 KB of shared memory, so two CTAs share an SM and one's
+// products run under the other's decays; X is fetched into the buffers of b and c before their first tiles.
+constexpr int kMapThreads = 160;
+template <int D> struct MapSmem {
+  static constexpr int tile = TM * D * 2, panel = TM * 128;
+  // below 77 KB a third CTA would fit the shared memory but not the tensor memory
+  static constexpr int bytes = 1024 + (3 * tile < 78 * 1024 ? 78 * 1024 : 3 * tile);
+};
+
+struct MapMaps { CUtensorMap a, b, c, out; };
+
+// P of one group of 32 columns: s * factor(row, group) * col[cc], or on the diagonal block s * lam^|i-j|.
+template <int D, bool REV>
+__global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid_constant__ MapMaps maps, LinMapArgs a,
+                                                                   uint32_t* status) {
+  using L = MapSmem<D>;
+  extern __shared__ uint8_t dyn[];
+  __shared__ uint64_t bar_a, full_b, full_c, bar_s, bar_o, bar_p;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_slot;
+  __shared__ float diag[64];   // lam^n at 32 + n, zeros below: the diagonal blocks
+  uint8_t* as = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+  uint8_t* bs = as + L::tile;
+  uint8_t* cs = bs + L::tile;
+  volatile int* abort_flag = &abort_slot;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int64_t i0 = (int64_t)blockIdx.x * TM, len = item_tokens(a.lengths, b, a.N);
+  const int seg = (int)(i0 / kSeg);
+  const int64_t s0 = (int64_t)seg * kSeg, end = min(len, s0 + kSeg);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)b * a.N * a.H + h) * D;
+  if (i0 >= len) {   // behind the item's end: zeros
+    const int n = (int)min((int64_t)TM, a.N - i0) * (D / 8);
+    for (int i = tid; i < n; i += kMapThreads)
+      *reinterpret_cast<uint4*>(out + (i0 + i / (D / 8)) * a.H * D + (i % (D / 8)) * 8) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const bool has_state = a.initial || (REV ? seg != a.n_seg - 1 : seg != 0);
+  const int64_t j_first = REV ? i0 : s0;
+  const int n_tiles = (int)((REV ? end - i0 + TM - 1 : i0 - s0 + TM) / TM);
+  const float ld = a.log_decay[h];
+  if (tid == 0) {
+    mbar_init(&bar_a, 1);
+    mbar_init(&full_b, 1);
+    mbar_init(&full_c, 1);
+    mbar_init(&bar_s, 1);
+    mbar_init(&bar_o, 1);
+    mbar_init(&bar_p, 128);
+    abort_slot = 0;
+    fence_mbar_init();
+  }
+  if (tid < 64) diag[tid] = tid < 32 ? 0.f : decay_pow(ld, tid - 32);
+  if (warp == 4) { tmem_alloc(&tmem_slot, 256); tmem_relinquish(); }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tm_s = tmem_slot, tm_o = tm_s + 128;
+  bool ok = true;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      auto load = [&](uint8_t* dst, const CUtensorMap* m, int64_t tok, uint64_t* bar) {
+        mbar_arrive_expect_tx(bar, L::tile);
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) tma_load_4d(dst + p * L::panel, m, 64 * p, h, (int)tok, b, bar);
+      };
+      int nb = 0, nc = 0;   // loads issued into b's and c's buffers
+      load(as, &maps.a, i0, &bar_a);
+      if (has_state) {
+        const uint8_t* X = reinterpret_cast<const uint8_t*>(a.states + (((int64_t)b * a.H + h) * a.n_seg + seg) * D * D);
+        mbar_arrive_expect_tx(&full_b, D * D * 2);
+        bulk_g2s(bs, X, D * D * 2, &full_b);
+        mbar_arrive_expect_tx(&full_c, D * D * 2);
+        bulk_g2s(cs, X + D * D * 2, D * D * 2, &full_c);
+      } else {
+        load(bs, &maps.b, j_first, &full_b);
+        load(cs, &maps.c, j_first, &full_c);
+      }
+      ++nb, ++nc;
+      const uint32_t sa = smem_u32(as), sb = smem_u32(bs), sc = smem_u32(cs);
+      int no = 0, np = 0;   // phases of bar_o and bar_p that have been waited for
+      ok = wait_or_abort(&bar_a, 0, abort_flag);
+      if (has_state) {
+        ok = ok && wait_or_abort(&full_b, 0, abort_flag) && wait_or_abort(&full_c, 0, abort_flag);
+        if (ok) {
+          // X as stored has a's channel along rows; transposed, along columns
+          const uint32_t id = idesc_bf16(128, D, false, !a.transposed);
+          const uint64_t da = kdesc0(sa);
+          const uint64_t dh = a.transposed ? kdesc0(sb) : mdesc0(sb, D * 128), dl = a.transposed ? kdesc0(sc) : mdesc0(sc, D * 128);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t st = a.transposed ? kstep(k, D * 128) : mstep(k);
+            mma_ss(tm_o, da + kstep(k, L::panel), dh + st, id, k > 0);
+            mma_ss(tm_o, da + kstep(k, L::panel), dl + st, id, 1u);
+          }
+          mma_commit(&bar_o);
+          ok = wait_or_abort(&bar_o, no++ & 1, abort_flag);
+          if (ok) {
+            load(bs, &maps.b, j_first, &full_b);
+            load(cs, &maps.c, j_first, &full_c);
+            ++nb, ++nc;
+          }
+        }
+      }
+      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, D, false, true);
+      for (int t = 0; ok && t < n_tiles; ++t) {
+        if (t > 0) {   // P and c of the tile before have been read
+          ok = wait_or_abort(&bar_o, no++ & 1, abort_flag);
+          if (!ok) break;
+          load(cs, &maps.c, j_first + t * TM, &full_c);
+          ++nc;
+        }
+        ok = wait_or_abort(&full_b, (nb - 1) & 1, abort_flag);
+        if (!ok) break;
+        fence_after_sync();
+        const uint64_t da = kdesc0(sa), db = kdesc0(sb), dc = mdesc0(sc, L::panel);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) mma_ss(tm_s, da + kstep(k, L::panel), db + kstep(k, L::panel), id_s, k > 0);
+        mma_commit(&bar_s);
+        ok = wait_or_abort(&bar_s, t & 1, abort_flag);
+        if (!ok) break;
+        if (t + 1 < n_tiles) {
+          load(bs, &maps.b, j_first + (t + 1) * TM, &full_b);
+          ++nb;
+        }
+        if (t == 0 && has_state) ok = wait_or_abort(&bar_p, np++ & 1, abort_flag);   // O has been scaled
+        ok = ok && wait_or_abort(&bar_p, np++ & 1, abort_flag) && wait_or_abort(&full_c, (nc - 1) & 1, abort_flag);
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < TM / 16; ++k) mma_ts(tm_o, tm_s + 8 * k, dc + mstep(k), id_o, has_state || t || k);
+        mma_commit(&bar_o);
+      }
+      if (!ok) {   // copies in flight end before the CTA does
+        mbar_wait(&bar_a, 0, 100000000ull);
+        mbar_wait(&full_b, (nb - 1) & 1, 100000000ull);
+        mbar_wait(&full_c, (nc - 1) & 1, 100000000ull);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int row = tid;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    int no = 0;
+    if (has_state) {
+      const float w = decay_pow(ld, REV ? max((int64_t)0, end - 1 - (i0 + row)) : i0 + row - s0 + 1);
+      ok = warp_wait(&bar_o, no++ & 1, abort_flag);
+      if (ok) {
+        fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          uint32_t u[32];
+          tmem_ld32(tm_o + lanes + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * w);
+          tmem_st32(tm_o + lanes + c, u);
+        }
+        tmem_wait_st();
+        fence_before_sync();
+        mbar_arrive(&bar_p);
+      }
+    }
+    float col[32];   // lam^(31-cc), or lam^cc in the reverse direction
+#pragma unroll
+    for (int i = 0; i < 32; ++i) col[i] = diag[32 + (REV ? i : 31 - i)];
+    const bool ragged = len < a.N;
+    for (int t = 0; ok && t < n_tiles; ++t) {
+      const int64_t j0 = j_first + t * TM;
+      ok = warp_wait(&bar_s, t & 1, abort_flag);
+      if (!ok) break;
+      fence_after_sync();
+      const int off = (int)(REV ? j0 - i0 : i0 - j0);   // >= 0, a multiple of 128
+      const int n_valid = ragged ? (int)min((int64_t)TM, len - j0) : TM;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float s[32], p[16];
+        tmem_ld32(tm_s + lanes + 32 * g, s);
+        // distance from this row to the group's nearest column
+        const int near = REV ? off + 32 * g - row : off + row - 32 * g - 31;
+        const bool diagonal = off == 0 && g == warp, none = off == 0 && (REV ? g < warp : g > warp);
+        const float f = none || diagonal ? 0.f : decay_pow(ld, near);
+        tmem_wait_ld();
+        if (none) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] = 0.f;
+        } else {
+          if (diagonal) {
+            const float* d = diag + 32 + (REV ? -lane : lane);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = (REV ? i >= lane : i <= lane) ? s[i] * d[REV ? i : -i] : 0.f;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = s[i] * f * col[i];
+          }
+          if (n_valid < TM) {   // columns behind the item's end, whatever their scores
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = 32 * g + i < n_valid ? s[i] : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] = __uint_as_float(pack2(s[2 * i], s[2 * i + 1]));
+        }
+        tmem_st16(tm_s + lanes + 16 * g, p);
+      }
+      if (n_valid < TM) {   // c behind the end may hold anything, and 0 x NaN is NaN
+        ok = warp_wait(&full_c, (has_state + t) & 1, abort_flag);
+        for (int i = tid + n_valid * (D / 8); i < TM * (D / 8); i += 128)
+          *reinterpret_cast<uint4*>(cs + image_off(TM, i / (D / 8), i % (D / 8))) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async();
+      }
+      tmem_wait_st();
+      fence_before_sync();
+      mbar_arrive(&bar_p);
+    }
+    // O of the last tile: to bf16 in a's buffer, then out
+    if (ok) ok = warp_wait(&bar_o, (no + n_tiles - 1) & 1, abort_flag);
+    if (ok) {
+      fence_after_sync();
+      const bool live = i0 + row < len;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        float v[32];
+        tmem_ld32(tm_o + lanes + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          uint4 u;
+          u.x = pack2(v[i], v[i + 1]);
+          u.y = pack2(v[i + 2], v[i + 3]);
+          u.z = pack2(v[i + 4], v[i + 5]);
+          u.w = pack2(v[i + 6], v[i + 7]);
+          if (!live) u = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(as + image_off(TM, row, (c + i) / 8)) = u;
+        }
+      }
+      fence_proxy_async();
+    }
+    ok = named_sync_and(1, 128, ok);
+    if (ok && tid == 0) {
+#pragma unroll
+      for (int p = 0; p < D / 64; ++p) tma_store_4d(&maps.out, as + p * L::panel, 64 * p, h, (int)i0, b);
+      bulk_commit();
+      bulk_wait_read();
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (tid == 0 && *abort_flag) set_status(status, KDA_ERR_TIMEOUT);
+  fence_after_sync();
+  if (warp == 4) tmem_dealloc(tm_s, 256);
+}
+
+// [B][N][H][D] bf16 seen as a 4D tensor (channel, head, token, item); box: 64 channels x 1 head x `tokens` x 1 item.
+// Tokens past N and heads past H read as zero.
+bool encode(CUtensorMap* m, const void* base, const Dims& d, int tokens) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d.dk, (cuuint64_t)d.H, (cuuint64_t)d.N, (cuuint64_t)d.B};
+  const cuuint64_t strides[3] = {(cuuint64_t)d.dk * 2, (cuuint64_t)d.H * d.dk * 2, (cuuint64_t)d.N * d.H * d.dk * 2};
+  const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)tokens, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s) {
+  LocalMaps m;
+  if (!encode(&m.x, a.x, d, TL) || !encode(&m.y, a.y, d, TL)) return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(lin_tc_local_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLocalSmem);
+  if (e != cudaSuccess) return e;
+  const int groups = (d.H * D + 127) / 128;
+  lin_tc_local_kernel<D><<<dim3((unsigned)a.n_seg, groups, d.B), kLocalThreads, kLocalSmem, s>>>(m, a, status);
+  return cudaGetLastError();
+}
+
+template <int D, bool REV>
+cudaError_t map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s) {
+  MapMaps m;
+  if (!encode(&m.a, a.a, d, TM) || !encode(&m.b, a.b, d, TM) || !encode(&m.c, a.c, d, TM) || !encode(&m.out, a.out, d, TM))
+    return cudaErrorInvalidValue;
+  const cudaError_t e =
+      cudaFuncSetAttribute(lin_tc_map_kernel<D, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, MapSmem<D>::bytes);
+  if (e != cudaSuccess) return e;
+  lin_tc_map_kernel<D, REV><<<dim3((unsigned)((d.N + TM - 1) / TM), d.H, d.B), kMapThreads, MapSmem<D>::bytes, s>>>(m, a, status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int linear_tc_segment() { return kSeg; }
+
+cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s) {
+  return d.dk == 128 ? local<128>(d, a, status, s) : local<64>(d, a, status, s);
+}
+cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanArgs& a, bool local, cudaStream_t s) {
+  const dim3 grid(d.dk * d.dk / 8 / 128, d.B * d.H);
+  if (d.dk == 128) lin_tc_scan_kernel<128><<<grid, 128, 0, s>>>(a, local);
+  else lin_tc_scan_kernel<64><<<grid, 128, 0, s>>>(a, local);
+  return cudaGetLastError();
+}
+cudaError_t launch_linear_tc_map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s) {
+  if (d.dk == 128) return a.reverse ? map<128, true>(d, a, status, s) : map<128, false>(d, a, status, s);
+  return a.reverse ? map<64, true>(d, a, status, s) : map<64, false>(d, a, status, s);
+}
+
+}  // namespace kda

@@ -159,7 +159,7 @@ int kda_layernorm_bwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* d
 size_t kda_linear_workspace_bytes(const kda_problem* p, kda_dtype dtype) {
   kda::Dims d;
   if (make_shape(p, dtype, &d)) return 0;
-  return kStatusBytes + kda::linear_fwd_scratch(d);
+  return kStatusBytes + kda::linear_fwd_scratch(d, dtype);
 }
 
 int kda_linear_fwd(const kda_problem* p, kda_dtype dtype, const void* q, const void* k, const void* v,
@@ -173,20 +173,21 @@ int kda_linear_fwd(const kda_problem* p, kda_dtype dtype, const void* q, const v
   const Span sq{q, n}, sk{k, n}, sv{v, n}, sl{log_decay, (size_t)d.H * 4}, sn{lengths, (size_t)d.B * 4},
       s0{initial_state, m}, so{o, n}, sf{final_state, m};
   if ((st = check_aligned({sq, sk, sv, sl, so}, {sn, s0, sf}))) return st;
-  const size_t need = kStatusBytes + kda::linear_fwd_scratch(d);
+  const size_t need = kStatusBytes + kda::linear_fwd_scratch(d, dtype);
   if ((st = check_workspace(workspace, workspace_bytes, need))) return st;
   if ((st = check_alias({so, sf, {workspace, need}}, {sq, sk, sv, sl, sn, s0}))) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = cuda_status(cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s)))) return st;
   int launches = 0;
   return finish(kda::launch_linear_fwd(d, dtype, q, k, v, log_decay, lengths, initial_state, o, final_state,
-                                       static_cast<char*>(workspace) + kStatusBytes, s, &launches), launches);
+                                       static_cast<char*>(workspace) + kStatusBytes, static_cast<uint32_t*>(workspace), s,
+                                       &launches), launches);
 }
 
 size_t kda_linear_bwd_workspace_bytes(const kda_problem* p, kda_dtype dtype) {
   kda::Dims d;
   if (make_shape(p, dtype, &d)) return 0;
-  return kStatusBytes + kda::linear_bwd_scratch(d);
+  return kStatusBytes + kda::linear_bwd_scratch(d, dtype);
 }
 
 int kda_linear_bwd(const kda_problem* p, kda_dtype dtype, const void* q, const void* k, const void* v,
@@ -201,15 +202,15 @@ int kda_linear_bwd(const kda_problem* p, kda_dtype dtype, const void* q, const v
   const Span sq{q, n}, sk{k, n}, sv{v, n}, sl{log_decay, (size_t)d.H * 4}, sn{lengths, (size_t)d.B * 4},
       s0{initial_state, m}, sdo{d_o, n}, sdf{d_final_state, m}, odq{dq, n}, odk{dk, n}, odv{dv, n}, od0{d_initial_state, m};
   if ((st = check_aligned({sq, sk, sv, sl, sdo, odq, odk, odv}, {sn, s0, sdf, od0}))) return st;
-  const size_t need = kStatusBytes + kda::linear_bwd_scratch(d);
+  const size_t need = kStatusBytes + kda::linear_bwd_scratch(d, dtype);
   if ((st = check_workspace(workspace, workspace_bytes, need))) return st;
   if ((st = check_alias({odq, odk, odv, od0, {workspace, need}}, {sq, sk, sv, sl, sn, s0, sdo, sdf}))) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = cuda_status(cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s)))) return st;
   int launches = 0;
   return finish(kda::launch_linear_bwd(d, dtype, q, k, v, log_decay, lengths, initial_state, d_o, d_final_state, dq,
-                                       dk, dv, d_initial_state, static_cast<char*>(workspace) + kStatusBytes, s,
-                                       &launches), launches);
+                                       dk, dv, d_initial_state, static_cast<char*>(workspace) + kStatusBytes,
+                                       static_cast<uint32_t*>(workspace), s, &launches), launches);
 }
 
 int kda_linear_step(const kda_problem* p, kda_dtype dtype, const void* q, const void* k, const void* v,
