@@ -199,8 +199,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it (3 us), where this torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -375,25 +381,62 @@ def kda_bwd(p, q, k, v, log_alpha, beta, w_text, w_vis, d_o, dq, dk, dv, d_log_a
 # ---------------------------------------------------------------------------
 # operators beside the KDA scan: rotary positions, layer norm, linear attention with a decay per head
 # ---------------------------------------------------------------------------
-def _rope_call(where, p, r, q, k, inv_freq, q_out, k_out, positions, stream):
-    B, N, H, d, _ = _dims(p)
+def _addresses(where, specs, workspace=None, nbytes=0):
+    """Checks the arguments (name, tensor, elements, dtype) and returns their addresses.  A call in which all is well
+    costs one short look at each tensor; anything else goes through _Args, which passes or names it."""
+    out, device = [], -1
+    for name, t, n, dtype in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if type(t) is not torch.Tensor or not t.is_cuda or n == 0 or t.dtype is not dtype or t.numel() != n \
+                or not t.is_contiguous():
+            break
+        if device < 0:
+            device = torch.cuda.current_device()
+        if t.get_device() != device:
+            break
+        out.append(t.data_ptr())
+    else:
+        if workspace is None or type(workspace) is torch.Tensor and workspace.is_cuda and workspace.is_contiguous() \
+                and workspace.numel() * workspace.element_size() >= nbytes > 0 and workspace.get_device() == device:
+            return out
     a = _Args(where)
-    for n, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)):
-        a.add(n, t, B * N * H * d, (q.dtype,))
-    a.add("inv_freq", inv_freq, d // 2, (torch.float32,))
-    a.add("positions", positions, B * N * 3, (torch.int32,)).check_devices()
-    _check(getattr(_lib, where)(ctypes.byref(p), ctypes.byref(r), _dt(q.dtype), _ptr(q), _ptr(k), _ptr(inv_freq),
-                                _ptr(positions), _ptr(q_out), _ptr(k_out), _stream(stream)), where)
+    for name, t, n, dtype in specs:
+        a.add(name, t, n, (dtype,))
+    if workspace is not None and not isinstance(workspace, int):
+        a.add("workspace", workspace, 1, (workspace.dtype,), at_least=True)
+        if workspace.numel() * workspace.element_size() < nbytes:
+            a.fail(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, fewer than the "
+                   f"{nbytes} passed")
+    a.check_devices()
+    return [_ptr(t) for _, t, _, _ in specs]
+
+
+def _nbytes(workspace, workspace_bytes):
+    return workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+
+
+_F32, _I32 = torch.float32, torch.int32
+
+
+def _rope_call(where, call, p, r, q, k, inv_freq, q_out, k_out, positions, stream):
+    B, N, H, d, _ = _dims(p)
+    n, dt = B * N * H * d, q.dtype
+    q_, k_, f_, pos_, qo_, ko_ = _addresses(where, (
+        ("q", q, n, dt), ("k", k, n, dt), ("inv_freq", inv_freq, d // 2, _F32), ("positions", positions, B * N * 3, _I32),
+        ("q_out", q_out, n, dt), ("k_out", k_out, n, dt)))
+    _check(call(ctypes.byref(p), ctypes.byref(r), _dt(dt), q_, k_, f_, pos_, qo_, ko_, _stream(stream)), where)
 
 
 def kda_rope_fwd(p, r, q, k, inv_freq, q_out, k_out, positions=None, stream=None):
     """Rotary positions on q and k (k and k_out may be None); q_out and k_out may be q and k."""
-    _rope_call("kda_rope_fwd", p, r, q, k, inv_freq, q_out, k_out, positions, stream)
+    _rope_call("kda_rope_fwd", _lib.kda_rope_fwd, p, r, q, k, inv_freq, q_out, k_out, positions, stream)
 
 
 def kda_rope_bwd(p, r, d_q_out, d_k_out, inv_freq, dq, dk, positions=None, stream=None):
     """Gradients of q and k from those of kda_rope_fwd's outputs."""
-    _rope_call("kda_rope_bwd", p, r, d_q_out, d_k_out, inv_freq, dq, dk, positions, stream)
+    _rope_call("kda_rope_bwd", _lib.kda_rope_bwd, p, r, d_q_out, d_k_out, inv_freq, dq, dk, positions, stream)
 
 
 def _rows_cols(where, x):
@@ -404,13 +447,12 @@ def _rows_cols(where, x):
 
 def kda_layernorm_fwd(x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=None, stream=None):
     """Layer norm over x's last axis; weight, bias, mean and rstd are fp32 or None."""
-    rows, cols = _rows_cols("kda_layernorm_fwd", x)
-    f32 = (torch.float32,)
-    a = _Args("kda_layernorm_fwd").add("x", x, rows * cols, (x.dtype,)).add("y", y, rows * cols, (x.dtype,))
-    a.add("weight", weight, cols, f32).add("bias", bias, cols, f32)
-    a.add("mean", mean, rows, f32).add("rstd", rstd, rows, f32).check_devices()
-    _check(_lib.kda_layernorm_fwd(rows, cols, _dt(x.dtype), _ptr(x), _ptr(weight), _ptr(bias), eps, _ptr(y),
-                                  _ptr(mean), _ptr(rstd), _stream(stream)), "kda_layernorm_fwd")
+    where, dt = "kda_layernorm_fwd", x.dtype
+    rows, cols = _rows_cols(where, x)
+    x_, w_, b_, y_, m_, r_ = _addresses(where, (
+        ("x", x, rows * cols, dt), ("weight", weight, cols, _F32), ("bias", bias, cols, _F32), ("y", y, rows * cols, dt),
+        ("mean", mean, rows, _F32), ("rstd", rstd, rows, _F32)))
+    _check(_lib.kda_layernorm_fwd(rows, cols, _dt(dt), x_, w_, b_, eps, y_, m_, r_, _stream(stream)), where)
 
 
 def kda_layernorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
@@ -424,31 +466,18 @@ def alloc_layernorm_bwd_workspace(rows: int, cols: int, device="cuda") -> torch.
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _workspace_arg(a, workspace, nbytes):
-    if workspace is not None and not isinstance(workspace, int):
-        a.add("workspace", workspace, 1, (workspace.dtype,), at_least=True)
-        if workspace.numel() * workspace.element_size() < nbytes:
-            a.fail(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, fewer than the "
-                   f"{nbytes} passed")
-    return a
-
-
 def kda_layernorm_bwd(dy, x, mean, rstd, dx, workspace, weight=None, d_weight=None, d_bias=None, stream=None,
                       workspace_bytes=None):
     """Gradients of kda_layernorm_fwd: dx, and the sums d_weight and d_bias (either may be None)."""
-    rows, cols = _rows_cols("kda_layernorm_bwd", x)
-    nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
-    f32 = (torch.float32,)
-    a = _Args("kda_layernorm_bwd")
-    for n, t in (("dy", dy), ("x", x), ("dx", dx)):
-        a.add(n, t, rows * cols, (x.dtype,))
-    a.add("mean", mean, rows, f32).add("rstd", rstd, rows, f32)
-    for n, t in (("weight", weight), ("d_weight", d_weight), ("d_bias", d_bias)):
-        a.add(n, t, cols, f32)
-    _workspace_arg(a, workspace, nbytes).check_devices()
-    _check(_lib.kda_layernorm_bwd(rows, cols, _dt(x.dtype), _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
-                                  _ptr(dx), _ptr(d_weight), _ptr(d_bias), _ptr(workspace), nbytes, _stream(stream)),
-           "kda_layernorm_bwd")
+    where, dt = "kda_layernorm_bwd", x.dtype
+    rows, cols = _rows_cols(where, x)
+    n, nbytes = rows * cols, _nbytes(workspace, workspace_bytes)
+    dy_, x_, w_, m_, r_, dx_, dw_, db_ = _addresses(where, (
+        ("dy", dy, n, dt), ("x", x, n, dt), ("weight", weight, cols, _F32), ("mean", mean, rows, _F32),
+        ("rstd", rstd, rows, _F32), ("dx", dx, n, dt), ("d_weight", d_weight, cols, _F32), ("d_bias", d_bias, cols, _F32)),
+        workspace, nbytes)
+    _check(_lib.kda_layernorm_bwd(rows, cols, _dt(dt), dy_, x_, w_, m_, r_, dx_, dw_, db_, _ptr(workspace), nbytes,
+                                  _stream(stream)), where)
 
 
 def kda_linear_workspace_bytes(p: kda_problem, dtype) -> int:
@@ -473,47 +502,43 @@ def alloc_linear_bwd_workspace(p: kda_problem, dtype, device="cuda") -> torch.Te
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _linear_args(where, p, q, k, v, log_decay, lengths, acts, states, workspace=None, nbytes=0):
-    B, N, H, d, _ = _dims(p)
-    a = _Args(where)
-    for n, t in (("q", q), ("k", k), ("v", v)) + acts:
-        a.add(n, t, B * N * H * d, (q.dtype,))
-    a.add("log_decay", log_decay, H, (torch.float32,)).add("lengths", lengths, B, (torch.int32,))
-    for n, t in states:
-        a.add(n, t, B * H * d * d, (torch.float32,))
-    _workspace_arg(a, workspace, nbytes).check_devices()
-
-
 def kda_linear_fwd(p, q, k, v, log_decay, o, workspace, lengths=None, initial_state=None, final_state=None,
                    stream=None, workspace_bytes=None):
     """Linear attention with a fixed decay per head over whole sequences."""
-    nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
-    _linear_args("kda_linear_fwd", p, q, k, v, log_decay, lengths, (("o", o),),
-                 (("initial_state", initial_state), ("final_state", final_state)), workspace, nbytes)
-    _check(_lib.kda_linear_fwd(ctypes.byref(p), _dt(q.dtype), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                               _ptr(lengths), _ptr(initial_state), _ptr(o), _ptr(final_state), _ptr(workspace),
-                               nbytes, _stream(stream)), "kda_linear_fwd")
+    where, dt = "kda_linear_fwd", q.dtype
+    B, N, H, d, _ = _dims(p)
+    n, m, nbytes = B * N * H * d, B * H * d * d, _nbytes(workspace, workspace_bytes)
+    q_, k_, v_, l_, len_, s0_, o_, sn_ = _addresses(where, (
+        ("q", q, n, dt), ("k", k, n, dt), ("v", v, n, dt), ("log_decay", log_decay, H, _F32), ("lengths", lengths, B, _I32),
+        ("initial_state", initial_state, m, _F32), ("o", o, n, dt), ("final_state", final_state, m, _F32)), workspace, nbytes)
+    _check(_lib.kda_linear_fwd(ctypes.byref(p), _dt(dt), q_, k_, v_, l_, len_, s0_, o_, sn_, _ptr(workspace), nbytes,
+                               _stream(stream)), where)
 
 
 def kda_linear_bwd(p, q, k, v, log_decay, d_o, dq, dk, dv, workspace, lengths=None, initial_state=None,
                    d_final_state=None, d_initial_state=None, stream=None, workspace_bytes=None):
     """Gradients of kda_linear_fwd with respect to q, k, v and initial_state."""
-    nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
-    _linear_args("kda_linear_bwd", p, q, k, v, log_decay, lengths, (("d_o", d_o), ("dq", dq), ("dk", dk), ("dv", dv)),
-                 (("initial_state", initial_state), ("d_final_state", d_final_state),
-                  ("d_initial_state", d_initial_state)), workspace, nbytes)
-    _check(_lib.kda_linear_bwd(ctypes.byref(p), _dt(q.dtype), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                               _ptr(lengths), _ptr(initial_state), _ptr(d_o), _ptr(d_final_state), _ptr(dq),
-                               _ptr(dk), _ptr(dv), _ptr(d_initial_state), _ptr(workspace), nbytes, _stream(stream)),
-           "kda_linear_bwd")
+    where, dt = "kda_linear_bwd", q.dtype
+    B, N, H, d, _ = _dims(p)
+    n, m, nbytes = B * N * H * d, B * H * d * d, _nbytes(workspace, workspace_bytes)
+    q_, k_, v_, l_, len_, s0_, do_, dsn_, dq_, dk_, dv_, ds0_ = _addresses(where, (
+        ("q", q, n, dt), ("k", k, n, dt), ("v", v, n, dt), ("log_decay", log_decay, H, _F32), ("lengths", lengths, B, _I32),
+        ("initial_state", initial_state, m, _F32), ("d_o", d_o, n, dt), ("d_final_state", d_final_state, m, _F32),
+        ("dq", dq, n, dt), ("dk", dk, n, dt), ("dv", dv, n, dt), ("d_initial_state", d_initial_state, m, _F32)),
+        workspace, nbytes)
+    _check(_lib.kda_linear_bwd(ctypes.byref(p), _dt(dt), q_, k_, v_, l_, len_, s0_, do_, dsn_, dq_, dk_, dv_, ds0_,
+                               _ptr(workspace), nbytes, _stream(stream)), where)
 
 
 def kda_linear_step(p, q, k, v, log_decay, state_in, o, state_out, stream=None):
     """One token of the recurrence for every batch item and head; state_out may be state_in."""
-    _linear_args("kda_linear_step", p, q, k, v, log_decay, None, (("o", o),),
-                 (("state_in", state_in), ("state_out", state_out)))
-    _check(_lib.kda_linear_step(ctypes.byref(p), _dt(q.dtype), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                _ptr(state_in), _ptr(o), _ptr(state_out), _stream(stream)), "kda_linear_step")
+    where, dt = "kda_linear_step", q.dtype
+    B, N, H, d, _ = _dims(p)
+    n, m = B * N * H * d, B * H * d * d
+    q_, k_, v_, l_, si_, o_, so_ = _addresses(where, (
+        ("q", q, n, dt), ("k", k, n, dt), ("v", v, n, dt), ("log_decay", log_decay, H, _F32), ("state_in", state_in, m, _F32),
+        ("o", o, n, dt), ("state_out", state_out, m, _F32)))
+    _check(_lib.kda_linear_step(ctypes.byref(p), _dt(dt), q_, k_, v_, l_, si_, o_, so_, _stream(stream)), where)
 
 
 def kda_selftest_wait_timeout(p, q, k, v, log_alpha, beta, o, workspace, stage, wait_us, stream=None):

@@ -3,284 +3,415 @@
 //   mu = mean_c x,  r = (mean_c (x - mu)^2 + eps)^(-1/2),  h = (x - mu) r,  y = w h + b
 //   g = w dy:  dx = r (g - mean_c g - h mean_c (g h)),  dw = sum_rows dy h,  db = sum_rows dy
 //
-// Bound by memory: x in, y out (backward: dy and x in, dx out).  A row lives in the registers of the 1 to 32
-// warps that own it, so it is read once: the mean, then the squares around the mean (no cancellation), then
-// the output.  Columns of a thread are the same for every row it takes, so the backward pass sums dw and db
-// in registers over the rows of a persistent grid, writes one partial per row group, and a second launch adds
-// the partials in a fixed order: the result does not depend on timing.
+// Bound by memory: x in, y out (backward: dy and x in, dx out).  A row lives in the registers of the lanes that
+// own it, so it is read once: the mean, then the squares around the mean (no cancellation), then the output.
+// Columns of a thread are the same for every row it takes, so the backward pass sums dw and db in registers
+// over the rows of a persistent grid, writes one partial per CTA, and a second launch adds the partials in a
+// fixed order: the result does not depend on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 
 namespace kda {
 namespace {
 
-template <typename T, int V> struct Pack;   // V elements as one access
-template <> struct Pack<float, 4> { using U = uint4; };
-template <> struct Pack<__nv_bfloat16, 8> { using U = uint4; };
-template <> struct Pack<float, 1> { using U = float; };
-template <> struct Pack<__nv_bfloat16, 1> { using U = unsigned short; };
+// V elements as one access (16 bytes, 8, or one element): as fetched, and as fp32.
+template <typename T, int V> struct Raw;
+template <> struct Raw<float, 4> { using type = uint4; };
+template <> struct Raw<__nv_bfloat16, 8> { using type = uint4; };
+template <> struct Raw<__nv_bfloat16, 4> { using type = uint2; };
+template <typename T> struct Raw<T, 1> { using type = T; };
+template <typename T, int V> using raw_t = typename Raw<T, V>::type;
 
-template <typename T, int V> __device__ __forceinline__ void load_vec(const T* p, float* f) {
-  const typename Pack<T, V>::U u = *reinterpret_cast<const typename Pack<T, V>::U*>(p);
-  const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = to_f32(e[i]);
+__device__ __forceinline__ void widen(const uint4& u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
 }
-template <typename T, int V> __device__ __forceinline__ void store_vec(T* p, const float* f) {
-  typename Pack<T, V>::U u;
-  T* e = reinterpret_cast<T*>(&u);
+__device__ __forceinline__ void widen(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < V; ++i) e[i] = from_f32<T>(f[i]);
-  *reinterpret_cast<typename Pack<T, V>::U*>(p) = u;
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
 }
-// V fp32 parameters (weight, bias): 16-byte loads where V allows them.
-template <int V> __device__ __forceinline__ void load_par(const float* p, float* f) {
-  if constexpr (V % 4 == 0) {
+__device__ __forceinline__ void widen(const uint2& u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xffff0000u);
+  f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void widen(float u, float (&f)[1]) { f[0] = u; }
+__device__ __forceinline__ void widen(__nv_bfloat16 u, float (&f)[1]) { f[0] = __bfloat162float(u); }
+__device__ __forceinline__ void clear(uint2& u) { u = make_uint2(0, 0); }
+__device__ __forceinline__ void clear(uint4& u) { u = make_uint4(0, 0, 0, 0); }
+__device__ __forceinline__ void clear(float& u) { u = 0.f; }
+__device__ __forceinline__ void clear(__nv_bfloat16& u) { u = __nv_bfloat16(0.f); }
+template <int V> __device__ __forceinline__ void store_vec(float* p, const float (&f)[V]) {
+  if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  else p[0] = f[0];
+}
+template <int V> __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&f)[V]) {
+  if constexpr (V == 1) {
+    p[0] = __float2bfloat16_rn(f[0]);
+  } else {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = reinterpret_cast<const uint32_t&>(v);
+    }
+    if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
+}
+// V fp32 parameters (weight, bias); `none` where there are none.
+template <int V> __device__ __forceinline__ void load_par(const float* p, int c, float none, float (&f)[V]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = none;
+  } else if constexpr (V % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
-      const float4 u = *reinterpret_cast<const float4*>(p + i);
+      const float4 u = *reinterpret_cast<const float4*>(p + c + i);
       f[i] = u.x; f[i + 1] = u.y; f[i + 2] = u.z; f[i + 3] = u.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = p[i];
+    for (int i = 0; i < V; ++i) f[i] = p[c + i];
   }
 }
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-  return x;
-}
+// A row belongs to G lanes (a power of two, 8..1024) with E elements each, in vectors of V, and a group of lanes
+// takes R rows at a time: R rows' loads are in flight together and share one reading of the weight.
+template <int G> struct Shape {
+  static constexpr int threads = G < 128 ? 128 : G;
+  static constexpr int groups = threads / G;
+};
+constexpr int kFwdThreads = 1024, kBwdThreads = 512;   // resident threads per SM that registers must allow
+constexpr int ctas_of(int threads, int resident) { return threads < resident ? resident / threads : 1; }
 
-// Sum of K values over the W warps of a row (all threads of the CTA call it: rows of one CTA run in step).
-template <int W, int K>
-__device__ __forceinline__ void row_sum(float (&x)[K], float* scratch, int group, int wg) {
+// Sums of K values over the G lanes of a group; every thread of the CTA calls it.
+template <int G, int K>
+__device__ __forceinline__ void group_sum(float (&x)[K], float* scratch, int group, int lane) {
 #pragma unroll
-  for (int i = 0; i < K; ++i) x[i] = warp_sum(x[i]);
-  if constexpr (W > 1) {
+  for (int m = (G < 32 ? G : 32) / 2; m; m >>= 1)
+#pragma unroll
+    for (int i = 0; i < K; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], m);
+  if constexpr (G > 32) {
+    constexpr int W = G / 32;
     float* sc = scratch + group * W * K;
-    __syncthreads();   // the previous sums have been read
-    if ((threadIdx.x & 31) == 0) {
+    __syncthreads();   // the sums before have been read
+    if ((lane & 31) == 0) {
 #pragma unroll
-      for (int i = 0; i < K; ++i) sc[wg * K + i] = x[i];
+      for (int i = 0; i < K; ++i) sc[i * W + lane / 32] = x[i];
     }
     __syncthreads();
+    if constexpr (W <= 8) {
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-      float t = 0.f;
+      for (int i = 0; i < K; ++i) {
+        float t = sc[i * W];
 #pragma unroll
-      for (int w = 0; w < W; ++w) t += sc[w * K + i];
-      x[i] = t;
-    }
-  }
-}
-
-// W warps per row, E elements per thread in vectors of V.
-template <typename T, int V, int E, int W>
-struct Shape {
-  static constexpr int threads = W * 32 < 128 ? 128 : W * 32;
-  static constexpr int groups = threads / (W * 32);   // rows per CTA at a time
-};
-
-template <typename T, int V, int E, int W>
-__global__ void __launch_bounds__(Shape<T, V, E, W>::threads) norm_fwd_kernel(NormFwdArgs a) {
-  using S = Shape<T, V, E, W>;
-  __shared__ float scratch[S::groups * W];
-  const int group = threadIdx.x / (W * 32), lane = threadIdx.x % (W * 32), wg = lane / 32;
-  const int64_t row = (int64_t)blockIdx.x * S::groups + group;
-  const bool live = row < a.rows;
-  const T* x = static_cast<const T*>(a.x) + row * a.cols;
-  float v[E];
-#pragma unroll
-  for (int i = 0; i < E / V; ++i) {
-    const int c = (i * W * 32 + lane) * V;
-    if (live && c < a.cols) load_vec<T, V>(x + c, v + i * V);
-    else
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[i * V + j] = 0.f;
-  }
-  float s[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < E; ++i) s[0] += v[i];
-  row_sum<W>(s, scratch, group, wg);
-  const float mean = s[0] / (float)a.cols;
-  float q[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < E / V; ++i)
-    if ((i * W * 32 + lane) * V < a.cols)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float t = v[i * V + j] - mean;
-        q[0] += t * t;
+        for (int w = 1; w < W; ++w) t += sc[i * W + w];
+        x[i] = t;
       }
-  row_sum<W>(q, scratch, group, wg);
-  const float rstd = 1.f / sqrtf(q[0] / (float)a.cols + a.eps);
-  if (!live) return;
-  if (lane == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
-  }
-  T* y = static_cast<T*>(a.y) + row * a.cols;
+    } else {   // 16 or 32 partial sums: one per lane
 #pragma unroll
-  for (int i = 0; i < E / V; ++i) {
-    const int c = (i * W * 32 + lane) * V;
-    if (c >= a.cols) continue;
-    float w[V], b[V], o[V];
-    if (a.weight) load_par<V>(a.weight + c, w);
-    if (a.bias) load_par<V>(a.bias + c, b);
+      for (int i = 0; i < K; ++i) {
+        float t = sc[i * W + (lane & (W - 1))];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float h = (v[i * V + j] - mean) * rstd;
-      o[j] = (a.weight ? h * w[j] : h) + (a.bias ? b[j] : 0.f);
+        for (int m = W / 2; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+        x[i] = t;
+      }
     }
-    store_vec<T, V>(y + c, o);
   }
 }
 
-template <typename T, int V, int E, int W>
-__global__ void __launch_bounds__(Shape<T, V, E, W>::threads) norm_bwd_kernel(NormBwdArgs a) {
-  using S = Shape<T, V, E, W>;
-  __shared__ float scratch[S::groups * W * 2];
-  const int group = threadIdx.x / (W * 32), lane = threadIdx.x % (W * 32), wg = lane / 32;
-  const int64_t stride = (int64_t)gridDim.x * S::groups;
+// This lane's elements of rows row0 .. row0 + R - 1; zeros past the columns and the rows.
+template <typename T, int V, int E, int G, int R>
+__device__ __forceinline__ void fetch(const void* base, int64_t row0, int64_t rows, int cols, int lane,
+                                      raw_t<T, V> (&v)[R][E / V]) {
+  const T* p = static_cast<const T*>(base) + row0 * cols;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < E / V; ++i) {
+      const int c = (i * G + lane) * V;
+      if (row0 + r < rows && c < cols) v[r][i] = *reinterpret_cast<const raw_t<T, V>*>(p + (int64_t)r * cols + c);
+      else clear(v[r][i]);
+    }
+}
+
+// Forward: a row stays as fetched and is widened in each of the three passes over it: one instruction per element and
+// pass, against twice the registers.  A lane takes four columns at a time, whose weights and biases are one 16-byte
+// access each (of eight they would be two, half a line apart: the L1 cache, which serves them for every row, is then
+// 75% busy).  One row per group and many CTAs: 33,272 x 2048 bf16 in 51 us, against 57 with two rows at a time and 54
+// with a persistent grid that fetches ahead; fp32 runs at the bandwidth of a copy either way (84 us).
+template <typename T, int V, int NV, int G, int R>
+__global__ void __launch_bounds__(Shape<G>::threads, ctas_of(Shape<G>::threads, kFwdThreads)) norm_fwd_kernel(NormFwdArgs a) {
+  using S = Shape<G>;
+  __shared__ float scratch[S::groups * (G / 32 + 1) * R];
+  const int group = threadIdx.x / G, lane = threadIdx.x % G;
   const float inv = 1.f / (float)a.cols;
-  float w[E], dw[E], db[E];
+  const int64_t row0 = ((int64_t)blockIdx.x * S::groups + group) * R;
+  raw_t<T, V> cur[R][NV];
+  fetch<T, V, V * NV, G, R>(a.x, row0, a.rows, a.cols, lane, cur);
+  float s[R], mean[R];
 #pragma unroll
-  for (int i = 0; i < E; ++i) w[i] = 1.f, dw[i] = 0.f, db[i] = 0.f;
-  if (a.weight) {
+  for (int r = 0; r < R; ++r) {
+    s[r] = 0.f;
 #pragma unroll
-    for (int i = 0; i < E / V; ++i) {
-      const int c = (i * W * 32 + lane) * V;
-      if (c < a.cols) load_par<V>(a.weight + c, w + i * V);
+    for (int i = 0; i < NV; ++i) {
+      float v[V];
+      widen(cur[r][i], v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[r] += v[j];
     }
   }
-  for (int64_t row0 = (int64_t)blockIdx.x * S::groups; row0 < a.rows; row0 += stride) {
-    const int64_t row = row0 + group;
-    const bool live = row < a.rows;
-    const T* x = static_cast<const T*>(a.x) + row * a.cols;
-    const T* dy = static_cast<const T*>(a.dy) + row * a.cols;
-    float h[E], g[E];
+  group_sum<G>(s, scratch, group, lane);
 #pragma unroll
-    for (int i = 0; i < E / V; ++i) {
-      const int c = (i * W * 32 + lane) * V;
-      if (live && c < a.cols) {
-        load_vec<T, V>(x + c, h + i * V);
-        load_vec<T, V>(dy + c, g + i * V);
-      } else {
+  for (int r = 0; r < R; ++r) {
+    mean[r] = s[r] * inv;
+    s[r] = 0.f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) h[i * V + j] = 0.f, g[i * V + j] = 0.f;
+    for (int i = 0; i < NV; ++i)
+      if ((i * G + lane) * V < a.cols) {
+        float v[V];
+        widen(cur[r][i], v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = v[j] - mean[r];
+          s[r] = fmaf(d, d, s[r]);
+        }
+      }
+  }
+  group_sum<G>(s, scratch, group, lane);
+#pragma unroll
+  for (int r = 0; r < R; ++r) s[r] = 1.f / sqrtf(fmaf(s[r], inv, a.eps));
+  if (lane == 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (row0 + r < a.rows) {
+        if (a.mean) a.mean[row0 + r] = mean[r];
+        if (a.rstd) a.rstd[row0 + r] = s[r];
+      }
+  }
+  T* y = static_cast<T*>(a.y) + row0 * a.cols;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * G + lane) * V;
+    if (c >= a.cols) continue;
+    float w[V], b[V];
+    load_par<V>(a.weight, c, 1.f, w);
+    load_par<V>(a.bias, c, 0.f, b);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (row0 + r >= a.rows) break;
+      float v[V], o[V];
+      widen(cur[r][i], v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = fmaf((v[j] - mean[r]) * s[r], w[j], b[j]);
+      store_vec<V>(y + (int64_t)r * a.cols + c, o);
+    }
+  }
+}
+
+// Backward: a persistent grid; the rows of the next turn are fetched before the sums of this one, so the loads do not
+// wait for reductions and stores.
+template <typename T, int V, int E, int G, int R>
+__global__ void __launch_bounds__(Shape<G>::threads, ctas_of(Shape<G>::threads, kBwdThreads)) norm_bwd_kernel(NormBwdArgs a) {
+  using S = Shape<G>;
+  constexpr int NV = E / V;
+  __shared__ float scratch[S::groups * (G / 32 + 1) * 2 * R];
+  __shared__ float sums[S::groups > 1 ? S::groups * G * E : 1];
+  const int group = threadIdx.x / G, lane = threadIdx.x % G;
+  const int64_t stride = (int64_t)gridDim.x * S::groups * R;
+  const float inv = 1.f / (float)a.cols;
+  float w[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * G + lane) * V;
+    load_par<V>(c < a.cols ? a.weight : nullptr, c, 1.f, w[i]);
+#pragma unroll
+    for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = 0.f;
+  }
+  raw_t<T, V> nx[R][NV], ny[R][NV];
+  float nm[R], nr[R];
+  auto get = [&](int64_t row0) {
+    fetch<T, V, E, G, R>(a.x, row0, a.rows, a.cols, lane, nx);
+    fetch<T, V, E, G, R>(a.dy, row0, a.rows, a.cols, lane, ny);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool live = row0 + r < a.rows;
+      nm[r] = live ? a.mean[row0 + r] : 0.f;
+      nr[r] = live ? a.rstd[row0 + r] : 0.f;
+    }
+  };
+  get(((int64_t)blockIdx.x * S::groups + group) * R);
+  for (int64_t base = (int64_t)blockIdx.x * S::groups * R; base < a.rows; base += stride) {
+    const int64_t row0 = base + group * R;
+    float h[R][NV][V], g[R][NV][V], rstd[R], s[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float mean = nm[r];
+      rstd[r] = nr[r];
+      s[2 * r] = s[2 * r + 1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        widen(nx[r][i], h[r][i]);
+        widen(ny[r][i], g[r][i]);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {   // columns past the row have dy = 0
+          float& hh = h[r][i][j];
+          float& gg = g[r][i][j];
+          hh = (hh - mean) * rstd[r];
+          dw[i][j] = fmaf(gg, hh, dw[i][j]);
+          db[i][j] += gg;
+          gg *= w[i][j];
+          s[2 * r] += gg;
+          s[2 * r + 1] = fmaf(gg, hh, s[2 * r + 1]);
+        }
       }
     }
-    const float mean = live ? a.mean[row] : 0.f, rstd = live ? a.rstd[row] : 0.f;
-    float s[2] = {0.f, 0.f};
+    get(row0 + stride);
+    group_sum<G>(s, scratch, group, lane);
+    T* dx = static_cast<T*>(a.dx) + row0 * a.cols;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {   // columns past the row have g = 0
-      h[i] = (h[i] - mean) * rstd;
-      dw[i] += g[i] * h[i];
-      db[i] += g[i];
-      g[i] *= w[i];
-      s[0] += g[i];
-      s[1] += g[i] * h[i];
-    }
-    row_sum<W>(s, scratch, group, wg);
-    if (!live) continue;
-    const float mg = s[0] * inv, mgh = s[1] * inv;
-    T* dx = static_cast<T*>(a.dx) + row * a.cols;
+    for (int r = 0; r < R; ++r) {
+      if (row0 + r >= a.rows) break;
+      const float mg = -s[2 * r] * inv * rstd[r], mgh = -s[2 * r + 1] * inv * rstd[r];
 #pragma unroll
-    for (int i = 0; i < E / V; ++i) {
-      const int c = (i * W * 32 + lane) * V;
-      if (c >= a.cols) continue;
-      float o[V];
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * G + lane) * V;
+        if (c >= a.cols) continue;
+        float o[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = rstd * (g[i * V + j] - mg - h[i * V + j] * mgh);
-      store_vec<T, V>(dx + c, o);
+        for (int j = 0; j < V; ++j) o[j] = fmaf(g[r][i][j], rstd[r], fmaf(h[r][i][j], mgh, mg));
+        store_vec<V>(dx + (int64_t)r * a.cols + c, o);
+      }
     }
   }
   if (!a.parts) return;
-  float* part = a.parts + ((int64_t)blockIdx.x * S::groups + group) * 2 * a.cols;
+  float* part = a.parts + (int64_t)blockIdx.x * 2 * a.cols;
 #pragma unroll
-  for (int i = 0; i < E / V; ++i) {
-    const int c = (i * W * 32 + lane) * V;
-    if (c >= a.cols) continue;
+  for (int which = 0; which < 2; ++which) {   // the CTA's groups, added in order
+    float(&acc)[NV][V] = which ? db : dw;
+    if constexpr (S::groups > 1) {
+      __syncthreads();
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      part[c + j] = dw[i * V + j];
-      part[a.cols + c + j] = db[i * V + j];
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) sums[(group * NV * V + i * V + j) * G + lane] = acc[i][j];
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            for (int k = 1; k < S::groups; ++k) acc[i][j] += sums[(k * NV * V + i * V + j) * G + lane];
+      }
+    }
+    if (group == 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * G + lane) * V;
+        if (c >= a.cols) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) part[which * a.cols + c + j] = acc[i][j];
+      }
     }
   }
 }
 
-// Adds the partials of 32 columns: 8 strands of rows, joined in a fixed order.
-__global__ void __launch_bounds__(256) norm_sum_kernel(const float* parts, int n_parts, int cols, float* dw, float* db) {
-  __shared__ float sm[8][32];
+// Adds the partials of 32 columns: 32 strands of rows, joined in a fixed order.
+__global__ void __launch_bounds__(1024) norm_sum_kernel(const float* parts, int n_parts, int cols, float* dw, float* db) {
+  __shared__ float sm[32][33];
   const int cx = threadIdx.x % 32, ry = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + cx;   // over 2 * cols: the weight's sums, then the bias's
   float s = 0.f;
-  if (c < 2 * cols)
-    for (int r = ry; r < n_parts; r += 8) s += parts[(int64_t)r * 2 * cols + c];
+  if (c < 2 * cols) {
+#pragma unroll 4
+    for (int r = ry; r < n_parts; r += 32) s += parts[(int64_t)r * 2 * cols + c];
+  }
   sm[ry][cx] = s;
   __syncthreads();
-  if (ry || c >= 2 * cols) return;
+  float t = sm[cx][ry];   // warp ry adds column ry
 #pragma unroll
-  for (int r = 1; r < 8; ++r) s += sm[r][cx];
-  if (c < cols) { if (dw) dw[c] = s; }
-  else if (db) db[c - cols] = s;
+  for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+  const int k = blockIdx.x * 32 + ry;
+  if (cx || k >= 2 * cols) return;
+  if (k < cols) { if (dw) dw[k] = t; }
+  else if (db) db[k - cols] = t;
 }
 
-constexpr int kFwdE = 32, kBwdE = 16;   // elements of a row per thread
+template <int N> using Const = std::integral_constant<int, N>;
 
-int warps_for(int cols, int e) {
-  int w = 1;
-  while (w * 32 * e < cols) w *= 2;
-  return w;
+template <typename T, int V, int NV, int G, int R>
+cudaError_t fwd_shape(const NormFwdArgs& a, cudaStream_t s) {
+  using S = Shape<G>;
+  constexpr int per = S::groups * R;
+  norm_fwd_kernel<T, V, NV, G, R><<<(unsigned)((a.rows + per - 1) / per), S::threads, 0, s>>>(a);
+  return cudaGetLastError();
 }
-
+// Vectors of a row: up to 4 per lane and 32 lanes, then 8 (scalars: 16) per lane, then more warps.  Narrow rows come
+// in pairs, which keeps 64 bytes per lane in flight and shares a reading of the weights.
 template <typename T, int V>
 cudaError_t fwd(const NormFwdArgs& a, cudaStream_t s) {
-  const int W = warps_for(a.cols, kFwdE);
-  auto go = [&](auto kernel, int threads, int groups) {
-    kernel<<<(unsigned)((a.rows + groups - 1) / groups), threads, 0, s>>>(a);
-    return cudaGetLastError();
-  };
-#define KDA_NORM(w) \
-  case w: return go(norm_fwd_kernel<T, V, kFwdE, w>, Shape<T, V, kFwdE, w>::threads, Shape<T, V, kFwdE, w>::groups)
-  switch (W) {
-    KDA_NORM(1);
-    KDA_NORM(2);
-    KDA_NORM(4);
-    KDA_NORM(8);
-    KDA_NORM(16);
+  const int n = (a.cols + V - 1) / V;
+  if (n <= 8) return fwd_shape<T, V, 1, 8, 4>(a, s);
+  if (n <= 16) return fwd_shape<T, V, 2, 8, 2>(a, s);
+  if (n <= 32) return fwd_shape<T, V, 4, 8, 2>(a, s);
+  if (n <= 64) return fwd_shape<T, V, 4, 16, 2>(a, s);
+  if (n <= 128) return fwd_shape<T, V, 4, 32, 2>(a, s);
+  if (n <= 256) return fwd_shape<T, V, 8, 32, 1>(a, s);
+  if (n <= 512) return fwd_shape<T, V, 8, 64, 1>(a, s);
+  if (n <= 1024) return fwd_shape<T, V, 8, 128, 1>(a, s);
+  if (n <= 2048) return fwd_shape<T, V, 8, 256, 1>(a, s);
+  if (n <= 4096) return fwd_shape<T, V, 8, 512, 1>(a, s);
+  if constexpr (V == 1) {
+    if (n <= 8192) return fwd_shape<T, V, 16, 512, 1>(a, s);
+    return fwd_shape<T, V, 16, 1024, 1>(a, s);
   }
-#undef KDA_NORM
   return cudaErrorInvalidValue;
 }
 
-template <typename T, int V>
-cudaError_t bwd(const NormBwdArgs& a, int grid, cudaStream_t s) {
-  const int W = warps_for(a.cols, kBwdE);
-#define KDA_NORM(w) \
-  case w: norm_bwd_kernel<T, V, kBwdE, w><<<grid, Shape<T, V, kBwdE, w>::threads, 0, s>>>(a); return cudaGetLastError()
-  switch (W) {
-    KDA_NORM(1);
-    KDA_NORM(2);
-    KDA_NORM(4);
+// Backward: 16 elements of a row per lane and one row at a time (33,272 x 2048 bf16: 82 us; 8 and two rows 83 us, the
+// reductions then cost a third of the instructions; 16 and two rows 151 us, out of registers).  Scalar accesses take
+// 8 and two rows (2047 columns: 116 us against 160).
+int lanes_for(int cols, int e) {
+  int g = 8;
+  while (g < 1024 && g * e < cols) g *= 2;
+  return g;
+}
+constexpr int groups_for(int g) { return g < 128 ? 128 / g : 1; }
+
+template <typename T, int V, int E, int R>
+cudaError_t bwd_shape(const NormBwdArgs& a, int grid, cudaStream_t s) {
+#define KDA_NORM(g) \
+  case g: norm_bwd_kernel<T, V, E, g, R><<<grid, Shape<g>::threads, 0, s>>>(a); break
+  switch (lanes_for(a.cols, E)) {
     KDA_NORM(8);
     KDA_NORM(16);
     KDA_NORM(32);
+    KDA_NORM(64);
+    KDA_NORM(128);
+    KDA_NORM(256);
+    KDA_NORM(512);
+    KDA_NORM(1024);
   }
 #undef KDA_NORM
-  return cudaErrorInvalidValue;
+  return cudaGetLastError();
 }
-
-int bwd_groups(int cols) { return std::max(1, 4 / warps_for(cols, kBwdE)); }
+template <typename T, int V>
+cudaError_t bwd(const NormBwdArgs& a, int grid, cudaStream_t s) {
+  if constexpr (V == 1)
+    if (a.cols <= 8 * 512) return bwd_shape<T, V, 8, 2>(a, grid, s);
+  return bwd_shape<T, V, 16, 1>(a, grid, s);
+}
 
 // CTAs of the backward pass: enough to fill the GPU, no more than there are row groups.
 int bwd_grid(int64_t rows, int cols) {
-  const int threads = std::max(128, 32 * warps_for(cols, kBwdE));
-  const int64_t need = (rows + bwd_groups(cols) - 1) / bwd_groups(cols);
-  return (int)std::min<int64_t>(need, (int64_t)148 * (1024 / threads));
+  // lanes for 16 elements each; scalar rows have twice as many lanes and rows per turn, so as many groups' rows
+  const int g = lanes_for(cols, 16), threads = std::max(128, g), per = groups_for(g);
+  return (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)148 * ctas_of(threads, kBwdThreads));
 }
 
 }  // namespace
@@ -288,14 +419,14 @@ int bwd_grid(int64_t rows, int cols) {
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, kda_dtype dt, cudaStream_t s, int* launches) {
   if (a.rows == 0) return cudaSuccess;
   cudaError_t e;
-  if (dt == KDA_DT_BF16) e = a.cols % 8 == 0 ? fwd<__nv_bfloat16, 8>(a, s) : fwd<__nv_bfloat16, 1>(a, s);
+  if (dt == KDA_DT_BF16) e = a.cols % 4 == 0 ? fwd<__nv_bfloat16, 4>(a, s) : fwd<__nv_bfloat16, 1>(a, s);
   else e = a.cols % 4 == 0 ? fwd<float, 4>(a, s) : fwd<float, 1>(a, s);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
 
 size_t norm_bwd_parts(int64_t rows, int cols) {
-  return (size_t)bwd_grid(rows, cols) * bwd_groups(cols) * 2 * cols * sizeof(float);
+  return (size_t)bwd_grid(rows, cols) * 2 * cols * sizeof(float);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, kda_dtype dt, float* dw, float* db, cudaStream_t s, int* launches) {
@@ -311,7 +442,7 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& a, kda_dtype dt, float* dw, float
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (!dw && !db) return cudaSuccess;
-  norm_sum_kernel<<<(2 * a.cols + 31) / 32, 256, 0, s>>>(a.parts, grid * bwd_groups(a.cols), a.cols, dw, db);
+  norm_sum_kernel<<<(2 * a.cols + 31) / 32, 1024, 0, s>>>(a.parts, grid, a.cols, dw, db);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   *launches += 1;
   return cudaSuccess;

@@ -16,7 +16,7 @@
 // mma.sync in tf32 with each operand split into two terms (three products, 2^-22 relative): fp32 accuracy.
 // Decays are lam^n = exp(n log lam) of whole n >= 0: never above 1, so nothing overflows however fast a head
 // forgets, and the fp32 error of n log lam, 2^-25 |n log lam|, is largest beside e^-1.
-#include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 

@@ -18,79 +18,89 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;   // vectors in flight per thread and half
 
-// Elements of one 16-byte vector.
+// 16 bytes as fp32 values and back (bf16 in pairs: one instruction per element in, half of one out).
 template <typename T> struct Vec { static constexpr int n = 16 / sizeof(T); };
-
-template <typename T> __device__ __forceinline__ void unpack(const uint4& u, float* f) {
-  const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-  for (int i = 0; i < Vec<T>::n; ++i) f[i] = to_f32(e[i]);
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
 }
-template <typename T> __device__ __forceinline__ uint4 pack(const float* f) {
-  uint4 u;
-  T* e = reinterpret_cast<T*>(&u);
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < Vec<T>::n; ++i) e[i] = from_f32<T>(f[i]);
-  return u;
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = reinterpret_cast<const uint32_t&>(v);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // kHalves: pair j is (j, j + D/2); otherwise (2j, 2j + 1).
 template <typename T, int D, bool kHalves>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a) {
   constexpr int P = D / 2, TOK = kThreads / P, V = Vec<T>::n;
-  constexpr int UNITS = P / V;   // a unit: two vectors holding V whole pairs
-  __shared__ float2 turn[TOK * P];
-  const int tid = threadIdx.x;
-  const int64_t tok0 = (int64_t)blockIdx.x * TOK;
-  const int n_tok = (int)min((int64_t)TOK, a.tokens - tok0);
-  const int per_tok = a.n_tensors * a.H * UNITS;
-  const int items = n_tok * per_tok;
-
-  // item i: token, tensor, head, unit, innermost last
-  auto locate = [&](int i, int& tok, int& unit, const T*& src, T*& dst) {
-    tok = i / per_tok;
-    int r = i - tok * per_tok;
-    const int tensor = r >= a.H * UNITS;
-    r -= tensor * a.H * UNITS;
-    unit = r % UNITS;
-    const int64_t off = ((tok0 + tok) * a.H + r / UNITS) * D;
-    src = static_cast<const T*>(tensor ? a.x[1] : a.x[0]) + off;
-    dst = static_cast<T*>(tensor ? a.y[1] : a.y[0]) + off;
-  };
+  constexpr int UNITS = P / V;                   // a unit: two vectors holding V whole pairs
+  constexpr int LINES = kThreads / UNITS;        // lines (token, tensor, head) per sweep of the CTA
   constexpr int LO_STEP = kHalves ? V : 2 * V;   // first vector of unit u at u * LO_STEP
   constexpr int HI_OFF = kHalves ? P : V;        // the second one, from the first
-
-  for (int base = 0; base < items; base += kThreads * kUnroll) {
+  __shared__ float2 turn[TOK * P];
+  const int tid = threadIdx.x, unit = tid % UNITS;
+  const uint32_t tok0 = blockIdx.x * (uint32_t)TOK;
+  const int n_tok = min(TOK, (int)(a.tokens - tok0)), per_tok = a.n_tensors * a.H;
+  // this thread's next line: token tok, line r of its tensors' heads; offset of its first element
+  int tok = 0, r = tid / UNITS;
+  auto settle = [&] { while (r >= per_tok) r -= per_tok, ++tok; };
+  auto offset = [&](int& tensor) {
+    tensor = r >= a.H;
+    return ((int64_t)(tok0 + tok) * a.H + (tensor ? r - a.H : r)) * D + unit * LO_STEP;
+  };
+  settle();
+  bool first = true;
+  while (true) {
     uint4 lo[kUnroll], hi[kUnroll];
+    int64_t off[kUnroll];
+    int which[kUnroll];   // -1: no line; else 2 * token + tensor
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int i = base + u * kThreads + tid;
-      if (i >= items) continue;
-      int tok, unit;
-      const T* src;
-      T* dst;
-      locate(i, tok, unit, src, dst);
-      const uint4* s = reinterpret_cast<const uint4*>(src + unit * LO_STEP);
-      lo[u] = s[0];
-      hi[u] = s[HI_OFF / V];
-    }
-    if (base == 0) {   // the angles, while the first loads are in flight
-      const int tok = tid / P, j = tid % P;
+      which[u] = -1;
       if (tok < n_tok) {
+        int tensor;
+        off[u] = offset(tensor);
+        which[u] = 2 * tok + tensor;
+        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const T*>(tensor ? a.x[1] : a.x[0]) + off[u]);
+        lo[u] = s[0];
+        hi[u] = s[HI_OFF / V];
+        r += LINES;
+        settle();
+      }
+    }
+    if (first) {   // the angles, while the first loads are in flight
+      first = false;
+      const int j = tid % P;
+      if (tid / P < n_tok) {
         const int axis = j < a.pairs_t ? 0 : (j < a.pairs_t + a.pairs_h ? 1 : 2);
-        const int64_t t = tok0 + tok;
-        int64_t pos;
+        const uint32_t t = tok0 + tid / P;
+        double pos;
         if (a.positions) {
-          pos = a.positions[t * 3 + axis];
+          pos = (double)a.positions[(int64_t)t * 3 + axis];
         } else {
-          pos = t % a.N;
-          if (pos >= a.text) {
-            const int64_t m = pos - a.text;
-            const int64_t hw = (int64_t)a.Hg * a.Wg;
-            pos = a.text + (axis == 0 ? m / hw : (axis == 1 ? m % hw / a.Wg : m % a.Wg));
+          uint32_t n = t % (uint32_t)a.N;
+          if (n >= (uint32_t)a.text) {
+            const uint32_t m = n - (uint32_t)a.text, row = m / (uint32_t)a.Wg;
+            n = (uint32_t)a.text + (axis == 2 ? m - row * a.Wg : axis == 1 ? row % (uint32_t)a.Hg : row / (uint32_t)a.Hg);
           }
+          pos = (double)n;
         }
-        const double turns = (double)pos * ((double)a.inv_freq[j] * 0.15915494309189533577);   // 1 / (2 pi)
+        const double turns = pos * ((double)a.inv_freq[j] * 0.15915494309189533577);   // 1 / (2 pi)
         float sn, cs;
         sincospif(2.f * (float)(turns - rint(turns)), &sn, &cs);
         turn[tid] = make_float2(cs, a.inverse ? -sn : sn);
@@ -99,26 +109,34 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int i = base + u * kThreads + tid;
-      if (i >= items) continue;
-      int tok, unit;
-      const T* src;
-      T* dst;
-      locate(i, tok, unit, src, dst);
-      const float2* cs = turn + tok * P + unit * V;
-      float x[2 * V], y[2 * V];
-      unpack<T>(lo[u], x);
-      unpack<T>(hi[u], x + V);
+      if (which[u] < 0) continue;
+      const float4* cs = reinterpret_cast<const float4*>(turn + (which[u] >> 1) * P + unit * V);
+      float xl[V], xh[V], yl[V], yh[V];
+      unpack(lo[u], xl);
+      unpack(hi[u], xh);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int ia = kHalves ? j : 2 * j, ib = kHalves ? V + j : 2 * j + 1;
-        y[ia] = x[ia] * cs[j].x - x[ib] * cs[j].y;
-        y[ib] = x[ia] * cs[j].y + x[ib] * cs[j].x;
+      for (int j = 0; j < V; j += 2) {
+        const float4 t = cs[j / 2];   // cos, sin of pairs j and j + 1
+        if constexpr (kHalves) {
+          yl[j] = xl[j] * t.x - xh[j] * t.y;
+          yh[j] = xl[j] * t.y + xh[j] * t.x;
+          yl[j + 1] = xl[j + 1] * t.z - xh[j + 1] * t.w;
+          yh[j + 1] = xl[j + 1] * t.w + xh[j + 1] * t.z;
+        } else {   // pairs 0..V/2-1 in the first vector, the others in the second
+          float(&x)[V] = j < V / 2 ? xl : xh;
+          float(&y)[V] = j < V / 2 ? yl : yh;
+          const int i = 2 * j % V;
+          y[i] = x[i] * t.x - x[i + 1] * t.y;
+          y[i + 1] = x[i] * t.y + x[i + 1] * t.x;
+          y[i + 2] = x[i + 2] * t.z - x[i + 3] * t.w;
+          y[i + 3] = x[i + 2] * t.w + x[i + 3] * t.z;
+        }
       }
-      uint4* o = reinterpret_cast<uint4*>(dst + unit * LO_STEP);
-      o[0] = pack<T>(y);
-      o[HI_OFF / V] = pack<T>(y + V);
+      uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(which[u] & 1 ? a.y[1] : a.y[0]) + off[u]);
+      o[0] = pack(yl);
+      o[HI_OFF / V] = pack(yh);
     }
+    if (which[kUnroll - 1] < 0 || tok >= n_tok) break;
   }
 }
 
