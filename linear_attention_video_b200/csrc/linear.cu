@@ -52,6 +52,9 @@ __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], cons
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
+// The tensor cores truncate as they add to an accumulator, so a long chain drifts by 2^-24 per link; every 32-deep
+// product starts from zero (12 links) and is added to its running sum by an ordinary rounded addition.
+//
 // d += A B, both operands in two terms (lo lo, 2^-22 of the product, is left out).
 __device__ __forceinline__ void mma3(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float b0, float b1) {
   uint32_t bh[2], bl[2];
@@ -80,7 +83,9 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
 
 constexpr int TK = 32;       // tokens per shared-memory tile
 constexpr int TQ = 64;       // output rows per CTA
-constexpr int kSeg = 256;    // tokens per segment
+// Tokens per segment.  These kernels are bound by their products, and a token's share of them grows with the segment
+// (128: D + 64..128 columns of scores per row; 256: up to 256), while a state's traffic is small beside fp32 inputs.
+constexpr int kSeg = 128;
 
 // ---------------------------------------------------------------------------
 // a segment's own contribution: local[x][y] = sum_t w_t x_t y_t^T
@@ -115,17 +120,23 @@ __global__ void __launch_bounds__(256) lin_local_kernel(LinLocalArgs a) {
       *reinterpret_cast<float4*>(ys + r * LD + c) = fy;
     }
     __syncthreads();
+    uint32_t ah[TK / 8][4], al[TK / 8][4];
 #pragma unroll
     for (int k8 = 0; k8 < TK / 8; ++k8) {
       const float* xr = xs + (k8 * 8 + t) * LD + m0 + g;
       const float av[4] = {xr[0], xr[8], xr[4 * LD], xr[4 * LD + 8]};
-      uint32_t ah[4], al[4];
-      split4(av, ah, al);
+      split4(av, ah[k8], al[k8]);
+    }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n) {
+      float d[4] = {};
+#pragma unroll
+      for (int k8 = 0; k8 < TK / 8; ++k8) {
         const float* yr = ys + (k8 * 8 + t) * LD + n0 + n * 8 + g;
-        mma3(acc[n], ah, al, yr[0], yr[4 * LD]);
+        mma3(d, ah[k8], al[k8], yr[0], yr[4 * LD]);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[n][e] += d[e];
     }
   }
   float* out = a.local + (((int64_t)b * a.H + h) * a.n_seg + seg) * D * D;
@@ -185,21 +196,32 @@ __global__ void __launch_bounds__(128) lin_scan_kernel(LinScanArgs a) {
 // the map: out_i = lam^e(i) X^(T) a_i + sum_j lam^|i-j| (a_i . b_j) c_j over i's segment
 // ---------------------------------------------------------------------------
 template <int D> struct MapSmem {
-  static constexpr int LDA = D + 8;   // a, b: pairs of columns read as 8 bytes, rows 8 banks apart
-  static constexpr int LDC = D + 4;   // c: rows 2t read by lane t, 8 banks apart
-  static constexpr int floats = TQ * LDA + TK * LDA + TK * LDC + kSeg;
+  static constexpr int LDA = D + 8;    // a, b: pairs of columns read as 8 bytes, rows 8 banks apart
+  static constexpr int LDC = D + 4;    // c, X: rows 2t read by lane t, 8 banks apart
+  static constexpr int LDX = TK + 8;   // X transposed: D rows of 32 columns, read as b
+  static constexpr int stage = TK * LDA + TK * LDC;
+  static_assert(stage >= D * LDX, "");
+  static constexpr int floats = TQ * LDA + 2 * stage + kSeg;
   static constexpr int bytes = floats * (int)sizeof(float);
 };
 
+// 16 bytes global -> shared, zeros where `live` is false.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+// The state's D rows and then the segment's tokens pass through two stages of 32 rows each: 32 rows of X are a tile
+// of c whose scores are the rows of a themselves, scaled.  The k index of a product is permuted (2t, 2t+1 for t, t+4),
+// which makes the scores' accumulators A operands as they are.
 template <int D>
 __global__ void __launch_bounds__(128) lin_map_kernel(LinMapArgs a) {
   using L = MapSmem<D>;
-  constexpr int LDA = L::LDA, LDC = L::LDC, NT = D / 8;
+  constexpr int LDA = L::LDA, LDC = L::LDC, NT = D / 8, KT = TK / 8;
   extern __shared__ float sm[];
   float* as = sm;
-  float* bs = as + TQ * LDA;
-  float* cs = bs + TK * LDA;
-  float* pw = cs + TK * LDC;   // lam^n, n < kSeg
+  float* stages = as + TQ * LDA;
+  float* pw = stages + 2 * L::stage;   // lam^n, n < kSeg
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t i0 = (int64_t)blockIdx.x * TQ;
@@ -209,89 +231,118 @@ __global__ void __launch_bounds__(128) lin_map_kernel(LinMapArgs a) {
   const int64_t stride = (int64_t)a.H * D, off = (int64_t)b * a.N * stride + (int64_t)h * D;
   const float *pa = static_cast<const float*>(a.a) + off, *pb = static_cast<const float*>(a.b) + off,
               *pc = static_cast<const float*>(a.c) + off;
-  for (int i = tid; i < kSeg; i += 128) pw[i] = decay_pow(ld, i);
-  for (int i = tid; i < TQ * D / 4; i += 128) {
+  const bool has_state = i0 < end && (a.initial || (a.reverse ? seg != a.n_seg - 1 : seg != 0));
+  const float* X = a.n_seg == 1 ? a.initial + ((int64_t)b * a.H + h) * D * D
+                                : a.states + (((int64_t)b * a.H + h) * a.n_seg + seg) * D * D;
+  const int64_t jb = a.reverse ? i0 : s0, je = a.reverse ? end : min(end, i0 + TQ);
+  const int n_x = has_state ? D / TK : 0, n_kv = je > jb ? (int)((je - jb + TK - 1) / TK) : 0, n = n_x + n_kv;
+  auto fetch = [&](int u) {
+    float* bs = stages + (u & 1) * L::stage;
+    float* cs = bs + TK * LDA;
+    if (u >= n) {
+    } else if (u >= n_x) {
+      const int64_t j0 = jb + (int64_t)(u - n_x) * TK;
+      for (int i = tid; i < TK * D / 4; i += 128) {
+        const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+        const bool live = j0 + r < end;   // tokens behind the end: zeros, whatever stands there
+        const int64_t at = live ? (j0 + r) * stride + c : 0;
+        copy16(bs + r * LDA + c, pb + at, live);
+        copy16(cs + r * LDC + c, pc + at, live);
+      }
+    } else if (!a.transposed) {
+      for (int i = tid; i < TK * D / 4; i += 128) {
+        const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+        copy16(cs + r * LDC + c, X + (u * TK + r) * D + c, true);
+      }
+    } else {
+      for (int i = tid; i < TK * D / 4; i += 128) {
+        const int r = i / (TK / 4), c = (i % (TK / 4)) * 4;
+        copy16(bs + r * L::LDX + c, X + r * D + u * TK + c, true);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = tid; i < TQ * D / 4; i += 128) {   // rows behind the end: zero, and so is their output
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);   // rows behind the end: zero, and so is their output
-    if (i0 + r < end) f = load4(pa + (i0 + r) * stride + c);
-    *reinterpret_cast<float4*>(as + r * LDA + c) = f;
+    const bool live = i0 + r < end;
+    copy16(as + r * LDA + c, pa + (live ? (i0 + r) * stride + c : 0), live);
   }
+  fetch(0);
+  for (int i = tid; i < kSeg; i += 128) pw[i] = decay_pow(ld, i);
   const int r0 = warp * 16 + g;   // this thread's rows: r0 and r0 + 8
   float acc[NT][4] = {};
-  // the state's part: 32 rows of X at a time; the k index of a product is permuted (2t, 2t+1 for t, t+4)
-  const bool first = a.reverse ? seg == a.n_seg - 1 : seg == 0;
-  const float* X = a.n_seg == 1 ? a.initial : a.states;
-  if (X && i0 < end && !(first && !a.initial)) {
-    X += a.n_seg == 1 ? ((int64_t)b * a.H + h) * D * D : (((int64_t)b * a.H + h) * a.n_seg + seg) * D * D;
-    const float w0 = decay_pow(ld, a.reverse ? max((int64_t)0, end - 1 - (i0 + r0)) : i0 + r0 - s0 + 1);
-    const float w1 = decay_pow(ld, a.reverse ? max((int64_t)0, end - 1 - (i0 + r0 + 8)) : i0 + r0 + 8 - s0 + 1);
-    for (int k0 = 0; k0 < D; k0 += TK) {
-      __syncthreads();
-      if (!a.transposed) {
-        for (int i = tid; i < TK * D / 4; i += 128) {
-          const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-          *reinterpret_cast<float4*>(cs + r * LDC + c) = *reinterpret_cast<const float4*>(X + (k0 + r) * D + c);
-        }
-      } else {
-        for (int i = tid; i < TK * D; i += 128) cs[(i % TK) * LDC + i / TK] = X[(i / TK) * D + k0 + i % TK];
-      }
-      __syncthreads();
+  const float w0 = decay_pow(ld, a.reverse ? max((int64_t)0, end - 1 - (i0 + r0)) : i0 + r0 - s0 + 1);
+  const float w1 = decay_pow(ld, a.reverse ? max((int64_t)0, end - 1 - (i0 + r0 + 8)) : i0 + r0 + 8 - s0 + 1);
+  for (int u = 0; u < n; ++u) {
+    fetch(u + 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    const float* bs = stages + (u & 1) * L::stage;
+    const float* cs = bs + TK * LDA;
+    uint32_t ph[KT][4], pl[KT][4];
+    if (u < n_x) {
 #pragma unroll
-      for (int k8 = 0; k8 < TK / 8; ++k8) {
-        const float2 u = *reinterpret_cast<const float2*>(as + r0 * LDA + k0 + k8 * 8 + 2 * t);
-        const float2 v = *reinterpret_cast<const float2*>(as + (r0 + 8) * LDA + k0 + k8 * 8 + 2 * t);
-        const float av[4] = {u.x * w0, v.x * w1, u.y * w0, v.y * w1};
+      for (int k = 0; k < KT; ++k) {
+        const float2 x = *reinterpret_cast<const float2*>(as + r0 * LDA + u * TK + k * 8 + 2 * t);
+        const float2 y = *reinterpret_cast<const float2*>(as + (r0 + 8) * LDA + u * TK + k * 8 + 2 * t);
+        const float av[4] = {x.x * w0, y.x * w1, x.y * w0, y.y * w1};
+        split4(av, ph[k], pl[k]);
+      }
+    } else {
+      const int64_t j0 = jb + (int64_t)(u - n_x) * TK;
+      float p[KT][4] = {}, q[KT][4];
+#pragma unroll
+      for (int k8 = 0; k8 < D / 8; ++k8) {
+        if (k8 % 4 == 0) {
+#pragma unroll
+          for (int m = 0; m < KT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[m][e] = 0.f;
+        }
+        const float2 x = *reinterpret_cast<const float2*>(as + r0 * LDA + k8 * 8 + 2 * t);
+        const float2 y = *reinterpret_cast<const float2*>(as + (r0 + 8) * LDA + k8 * 8 + 2 * t);
+        const float av[4] = {x.x, y.x, x.y, y.y};
         uint32_t ah[4], al[4];
         split4(av, ah, al);
-        const float* cr = cs + (k8 * 8 + 2 * t) * LDC + g;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma3(acc[n], ah, al, cr[n * 8], cr[LDC + n * 8]);
+        for (int m = 0; m < KT; ++m) {
+          const float2 w = *reinterpret_cast<const float2*>(bs + (m * 8 + g) * LDA + k8 * 8 + 2 * t);
+          mma3(q[m], ah, al, w.x, w.y);
+        }
+        if (k8 % 4 == 3) {
+#pragma unroll
+          for (int m = 0; m < KT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[m][e] += q[m][e];
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < KT; ++m) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int ahead = (int)(i0 - j0) + r0 + (e / 2) * 8 - m * 8 - 2 * t - (e & 1);
+          const int dist = a.reverse ? -ahead : ahead;
+          p[m][e] = dist < 0 ? 0.f : p[m][e] * pw[dist];
+        }
+        const float av[4] = {p[m][0], p[m][2], p[m][1], p[m][3]};
+        split4(av, ph[m], pl[m]);
       }
     }
-  }
-  const int64_t jb = a.reverse ? i0 : s0, je = a.reverse ? end : min(end, i0 + TQ);
-  for (int64_t j0 = jb; j0 < je; j0 += TK) {
-    __syncthreads();
-    for (int i = tid; i < TK * D / 4; i += 128) {
-      const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-      float4 fb = make_float4(0.f, 0.f, 0.f, 0.f), fc = fb;
-      if (j0 + r < end) {
-        fb = load4(pb + (j0 + r) * stride + c);
-        fc = load4(pc + (j0 + r) * stride + c);
+    const bool as_b = u < n_x && a.transposed;   // X transposed lies as b does: columns 2t, 2t+1 of row n
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      float d[4] = {};
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        float2 w;
+        if (as_b) w = *reinterpret_cast<const float2*>(bs + (m * 8 + g) * L::LDX + k * 8 + 2 * t);
+        else w = make_float2(cs[(k * 8 + 2 * t) * LDC + m * 8 + g], cs[(k * 8 + 2 * t + 1) * LDC + m * 8 + g]);
+        mma3(d, ph[k], pl[k], w.x, w.y);
       }
-      *reinterpret_cast<float4*>(bs + r * LDA + c) = fb;
-      *reinterpret_cast<float4*>(cs + r * LDC + c) = fc;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[m][e] += d[e];
     }
-    __syncthreads();
-    float p[TK / 8][4] = {};
-#pragma unroll 4
-    for (int k8 = 0; k8 < D / 8; ++k8) {
-      const float2 u = *reinterpret_cast<const float2*>(as + r0 * LDA + k8 * 8 + 2 * t);
-      const float2 v = *reinterpret_cast<const float2*>(as + (r0 + 8) * LDA + k8 * 8 + 2 * t);
-      const float av[4] = {u.x, v.x, u.y, v.y};
-      uint32_t ah[4], al[4];
-      split4(av, ah, al);
-#pragma unroll
-      for (int n = 0; n < TK / 8; ++n) {
-        const float2 w = *reinterpret_cast<const float2*>(bs + (n * 8 + g) * LDA + k8 * 8 + 2 * t);
-        mma3(p[n], ah, al, w.x, w.y);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < TK / 8; ++n) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int dist0 = (int)(i0 - j0) + r0 + (e / 2) * 8 - n * 8 - 2 * t - (e & 1);
-        const int dist = a.reverse ? -dist0 : dist0;
-        p[n][e] = dist < 0 ? 0.f : p[n][e] * pw[dist];
-      }
-      const float av[4] = {p[n][0], p[n][2], p[n][1], p[n][3]};
-      uint32_t ah[4], al[4];
-      split4(av, ah, al);
-      const float* cr = cs + (n * 8 + 2 * t) * LDC + g;
-#pragma unroll
-      for (int m = 0; m < NT; ++m) mma3(acc[m], ah, al, cr[m * 8], cr[LDC + m * 8]);
-    }
+    __syncthreads();   // this stage is fetched into again
   }
   float* out = static_cast<float*>(a.out) + off;
 #pragma unroll
@@ -299,7 +350,7 @@ __global__ void __launch_bounds__(128) lin_map_kernel(LinMapArgs a) {
     const int64_t i = i0 + r0 + half * 8;
     if (i >= a.N) continue;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) store2(out + i * stride + n * 8 + 2 * t, acc[n][2 * half], acc[n][2 * half + 1]);
+    for (int m = 0; m < NT; ++m) store2(out + i * stride + m * 8 + 2 * t, acc[m][2 * half], acc[m][2 * half + 1]);
   }
 }
 
