@@ -41,6 +41,22 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return reinterpret_cast<const uint32_t&>(v);
 }
+// Two fp32 in one register pair, multiplied by one instruction.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t ab) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+  return pack2(a, b);
+}
 // a, b = bf16 pair + the rest
 __device__ __forceinline__ uint32_t take2(float& a, float& b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -322,7 +338,8 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
   __shared__ uint64_t bar_a, full_b, full_c, bar_s, bar_o, bar_p;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_slot;
-  __shared__ float diag[64];   // lam^n at 32 + n, zeros below: the diagonal blocks
+  __shared__ float diag[64];                // lam^n at 32 + n, zeros below
+  __shared__ float power32[4 * kSeg / TM];   // lam^(32 n)
   uint8_t* as = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   uint8_t* bs = as + L::tile;
   uint8_t* cs = bs + L::tile;
@@ -354,6 +371,7 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
     fence_mbar_init();
   }
   if (tid < 64) diag[tid] = tid < 32 ? 0.f : decay_pow(ld, tid - 32);
+  else if (tid < 64 + 4 * kSeg / TM) power32[tid - 64] = decay_pow(ld, 32 * (tid - 64));
   if (warp == 4) { tmem_alloc(&tmem_slot, 256); tmem_relinquish(); }
   fence_before_sync();
   __syncthreads();
@@ -451,7 +469,7 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
       ok = warp_wait(&bar_o, no++ & 1, abort_flag);
       if (ok) {
         fence_after_sync();
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float v[32];
           uint32_t u[32];
@@ -466,44 +484,50 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
         mbar_arrive(&bar_p);
       }
     }
-    float col[32];   // lam^(31-cc), or lam^cc in the reverse direction
+    uint64_t col[16];   // lam^(31-cc), or lam^cc in the reverse direction, in pairs
 #pragma unroll
-    for (int i = 0; i < 32; ++i) col[i] = diag[32 + (REV ? i : 31 - i)];
-    const bool ragged = len < a.N;
+    for (int i = 0; i < 16; ++i)
+      col[i] = REV ? pair2(diag[32 + 2 * i], diag[33 + 2 * i]) : pair2(diag[63 - 2 * i], diag[62 - 2 * i]);
+    // a row's distance to the nearest column of an earlier (later) group is rowf's plus a multiple of 32
+    const float rowf = decay_pow(ld, REV ? 32 - lane : lane + 1);
+    const int to_end = (int)min((int64_t)kSeg, len - j_first);   // tokens of the sequence from j_first on
     for (int t = 0; ok && t < n_tiles; ++t) {
-      const int64_t j0 = j_first + t * TM;
       ok = warp_wait(&bar_s, t & 1, abort_flag);
       if (!ok) break;
       fence_after_sync();
-      const int off = (int)(REV ? j0 - i0 : i0 - j0);   // >= 0, a multiple of 128
-      const int n_valid = ragged ? (int)min((int64_t)TM, len - j0) : TM;
-#pragma unroll
+      const int m = REV ? t : n_tiles - 1 - t;   // tiles between the rows and the columns
+      const int n_valid = to_end - t * TM;       // columns within the sequence (below TM at its end only)
+#pragma unroll 1
       for (int g = 0; g < 4; ++g) {
+        const int ahead = 4 * m + (REV ? g - warp : warp - g);   // groups from column to row
         float s[32], p[16];
         tmem_ld32(tm_s + lanes + 32 * g, s);
-        // distance from this row to the group's nearest column
-        const int near = REV ? off + 32 * g - row : off + row - 32 * g - 31;
-        const bool diagonal = off == 0 && g == warp, none = off == 0 && (REV ? g < warp : g > warp);
-        const float f = none || diagonal ? 0.f : decay_pow(ld, near);
         tmem_wait_ld();
-        if (none) {
+        if (ahead > 0) {
+          const float f = rowf * power32[ahead - 1];
+          const uint64_t ff = pair2(f, f);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            p[i] = __uint_as_float(pack2(mul2(pair2(s[2 * i], s[2 * i + 1]), mul2(ff, col[i]))));
+        } else if (ahead == 0) {
+          const float* d = diag + 32 + (REV ? -lane : lane);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {   // zeros of the table for columns that the row does not see
+            const float u = s[2 * i] * d[REV ? 2 * i : -2 * i], v = s[2 * i + 1] * d[REV ? 2 * i + 1 : -2 * i - 1];
+            p[i] = __uint_as_float(pack2((REV ? 2 * i >= lane : 2 * i <= lane) ? u : 0.f,
+                                         (REV ? 2 * i + 1 >= lane : 2 * i + 1 <= lane) ? v : 0.f));
+          }
+        } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) p[i] = 0.f;
-        } else {
-          if (diagonal) {
-            const float* d = diag + 32 + (REV ? -lane : lane);
+        }
+        if (n_valid < TM) {   // columns behind the end, whatever their scores
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = (REV ? i >= lane : i <= lane) ? s[i] * d[REV ? i : -i] : 0.f;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = s[i] * f * col[i];
+          for (int i = 0; i < 16; ++i) {
+            const int c = 32 * g + 2 * i;
+            const uint32_t keep = (c < n_valid ? 0xffffu : 0u) | (c + 1 < n_valid ? 0xffff0000u : 0u);
+            p[i] = __uint_as_float(__float_as_uint(p[i]) & keep);
           }
-          if (n_valid < TM) {   // columns behind the item's end, whatever their scores
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = 32 * g + i < n_valid ? s[i] : 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] = __uint_as_float(pack2(s[2 * i], s[2 * i + 1]));
         }
         tmem_st16(tm_s + lanes + 16 * g, p);
       }
@@ -522,7 +546,7 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
     if (ok) {
       fence_after_sync();
       const bool live = i0 + row < len;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float v[32];
         tmem_ld32(tm_o + lanes + c, v);
