@@ -8,14 +8,15 @@
 // column's place cc in its group of 32, lam^(i-j) = lam^(i - group's last) * lam^(31-cc), a factor per (row, group)
 // times one of 32 registers, both at most 1.  Only the 32 x 32 blocks on the diagonal look lam^(i-j) up.
 //
-// What is rounded: the decayed scores go to bf16 for their second product, as in any attention on these units
-// (2^-9 of each score at random, as much as the output's own rounding); a state enters a product as two bf16 terms
-// (16 bits), since the whole past of a slowly forgetting head passes through it; the sums that become a state are
-// taken of three bf16 terms (24 bits), because states are fp32 results.  All sums are fp32.
+// What is rounded: the decayed scores and the state that enters a segment go to bf16 for their products with c and a,
+// as in any attention on these units: each term of an output is rounded once, by at most 2^-8 of it (half a step),
+// like the output itself; together 1.4 times the output's own rounding at random.  The states stay fp32 from segment
+// to segment, and the sums that become a state are taken of three bf16 terms (24 bits), because states are fp32
+// results.  All sums are fp32.
 //
-// State images.  Between scan and map a state is two bf16 matrices (hi, lo) in the 128-byte-swizzled panels that
-// the tensor core reads, so a CTA fetches each with one bulk copy.  A segment's local state lies in the same
-// places, four fp32 where eight bf16 of hi will be and four where those of lo will be, so the scan works in place.
+// State images.  Between scan and map a state is a bf16 matrix in the 128-byte-swizzled panels that the tensor core
+// reads, so a CTA fetches it with one bulk copy.  Of a segment's fp32 local state, four of eight columns lie where
+// the image's eight will be and four as far behind it, so the scan works in place.
 #include "common.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
@@ -257,7 +258,7 @@ __device__ __forceinline__ Factor segment_factor(float log_decay, int64_t n) {
   return {hi, (float)(f - (double)hi)};
 }
 
-// A thread takes 8 columns of one row: 32 bytes of the local state, 16 each of the hi and lo images over them.
+// A thread takes 8 columns of one row: 32 bytes of the local state, 16 of the image over them.
 // local = false: nothing but the initial state enters (one segment, no final state wanted).
 template <int D>
 __global__ void __launch_bounds__(128) lin_tc_scan_kernel(LinScanArgs a, bool local) {
@@ -290,14 +291,7 @@ __global__ void __launch_bounds__(128) lin_tc_scan_kernel(LinScanArgs a, bool lo
       if (c0 + u >= a.n_seg) break;
       const int c = a.reverse ? a.n_seg - 1 - c0 - u : c0 + u;
       uint8_t* s = p + (int64_t)c * D * D * 4;
-      float t[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = S[i];
-      uint4 hi, lo;
-      hi.x = take2(t[0], t[1]); hi.y = take2(t[2], t[3]); hi.z = take2(t[4], t[5]); hi.w = take2(t[6], t[7]);
-      lo.x = pack2(t[0], t[1]); lo.y = pack2(t[2], t[3]); lo.z = pack2(t[4], t[5]); lo.w = pack2(t[6], t[7]);
-      *reinterpret_cast<uint4*>(s) = hi;
-      *reinterpret_cast<uint4*>(s + LO) = lo;
+      *reinterpret_cast<uint4*>(s) = make_uint4(pack2(S[0], S[1]), pack2(S[2], S[3]), pack2(S[4], S[5]), pack2(S[6], S[7]));
       if (c > last || !local) continue;   // behind the end: no tokens
       const Factor f = c == last ? part : whole;
       const float l[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
@@ -316,10 +310,12 @@ __global__ void __launch_bounds__(128) lin_tc_scan_kernel(LinScanArgs a, bool lo
 // map
 // ---------------------------------------------------------------------------
 // One CTA per 128 output rows: warps 0-3 hold a row per thread, one thread of warp 4 issues copies and products.
-//   O = a (Xhi + Xlo), scaled row by row by lam^e(i); then per tile of 128 tokens S = a b^T, P = bf16(S * decay)
-//   written over S in tensor memory, O += P c.
+//   O = a X, scaled row by row by lam^e(i); then per tile of 128 tokens S = a b^T, P = bf16(S * decay) written over
+//   S in tensor memory, O += P c.
 // S and O take 256 columns of tensor memory and a, b, c 96 KB of shared memory, so two CTAs share an SM and one's
-// products run under the other's decays; X is fetched into the buffers of b and c before their first tiles.
+// products run under the other's decays; X passes through c's buffer before c's first tile.  What was tried against
+// it: one persistent CTA with two lanes of 128 rows, copies fetched ahead and separate warps for the outputs, whose
+// larger code ran at the same speed (a fifth of the cycles waiting for instructions).
 constexpr int kMapThreads = 160;
 template <int D> struct MapSmem {
   static constexpr int tile = TM * D * 2, panel = TM * 128;
@@ -388,43 +384,19 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
       };
       int nb = 0, nc = 0;   // loads issued into b's and c's buffers
       load(as, &maps.a, i0, &bar_a);
+      load(bs, &maps.b, j_first, &full_b);
       if (has_state) {
-        const uint8_t* X = reinterpret_cast<const uint8_t*>(a.states + (((int64_t)b * a.H + h) * a.n_seg + seg) * D * D);
-        mbar_arrive_expect_tx(&full_b, D * D * 2);
-        bulk_g2s(bs, X, D * D * 2, &full_b);
         mbar_arrive_expect_tx(&full_c, D * D * 2);
-        bulk_g2s(cs, X + D * D * 2, D * D * 2, &full_c);
+        bulk_g2s(cs, a.states + (((int64_t)b * a.H + h) * a.n_seg + seg) * D * D, D * D * 2, &full_c);
       } else {
-        load(bs, &maps.b, j_first, &full_b);
         load(cs, &maps.c, j_first, &full_c);
       }
       ++nb, ++nc;
       const uint32_t sa = smem_u32(as), sb = smem_u32(bs), sc = smem_u32(cs);
-      int no = 0, np = 0;   // phases of bar_o and bar_p that have been waited for
-      ok = wait_or_abort(&bar_a, 0, abort_flag);
-      if (has_state) {
-        ok = ok && wait_or_abort(&full_b, 0, abort_flag) && wait_or_abort(&full_c, 0, abort_flag);
-        if (ok) {
-          // X as stored has a's channel along rows; transposed, along columns
-          const uint32_t id = idesc_bf16(128, D, false, !a.transposed);
-          const uint64_t da = kdesc0(sa);
-          const uint64_t dh = a.transposed ? kdesc0(sb) : mdesc0(sb, D * 128), dl = a.transposed ? kdesc0(sc) : mdesc0(sc, D * 128);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t st = a.transposed ? kstep(k, D * 128) : mstep(k);
-            mma_ss(tm_o, da + kstep(k, L::panel), dh + st, id, k > 0);
-            mma_ss(tm_o, da + kstep(k, L::panel), dl + st, id, 1u);
-          }
-          mma_commit(&bar_o);
-          ok = wait_or_abort(&bar_o, no++ & 1, abort_flag);
-          if (ok) {
-            load(bs, &maps.b, j_first, &full_b);
-            load(cs, &maps.c, j_first, &full_c);
-            ++nb, ++nc;
-          }
-        }
-      }
+      const uint64_t da = kdesc0(sa), db = kdesc0(sb), dc = mdesc0(sc, L::panel);
       constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, D, false, true);
+      int no = 0;   // phases of bar_o that have been waited for
+      ok = wait_or_abort(&bar_a, 0, abort_flag);
       for (int t = 0; ok && t < n_tiles; ++t) {
         if (t > 0) {   // P and c of the tile before have been read
           ok = wait_or_abort(&bar_o, no++ & 1, abort_flag);
@@ -435,18 +407,33 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
         ok = wait_or_abort(&full_b, (nb - 1) & 1, abort_flag);
         if (!ok) break;
         fence_after_sync();
-        const uint64_t da = kdesc0(sa), db = kdesc0(sb), dc = mdesc0(sc, L::panel);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) mma_ss(tm_s, da + kstep(k, L::panel), db + kstep(k, L::panel), id_s, k > 0);
         mma_commit(&bar_s);
+        if (t == 0 && has_state) {
+          ok = wait_or_abort(&full_c, 0, abort_flag);
+          if (!ok) break;
+          // X as stored has a's channel along rows; transposed, along columns
+          const uint32_t id = idesc_bf16(128, D, false, !a.transposed);
+          const uint64_t dx = a.transposed ? kdesc0(sc) : mdesc0(sc, D * 128);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tm_o, da + kstep(k, L::panel), dx + (a.transposed ? kstep(k, D * 128) : mstep(k)), id, k > 0);
+          mma_commit(&bar_o);
+        }
         ok = wait_or_abort(&bar_s, t & 1, abort_flag);
         if (!ok) break;
         if (t + 1 < n_tiles) {
           load(bs, &maps.b, j_first + (t + 1) * TM, &full_b);
           ++nb;
         }
-        if (t == 0 && has_state) ok = wait_or_abort(&bar_p, np++ & 1, abort_flag);   // O has been scaled
-        ok = ok && wait_or_abort(&bar_p, np++ & 1, abort_flag) && wait_or_abort(&full_c, (nc - 1) & 1, abort_flag);
+        if (t == 0 && has_state) {
+          ok = wait_or_abort(&bar_o, no++ & 1, abort_flag);
+          if (!ok) break;
+          load(cs, &maps.c, j_first, &full_c);
+          ++nc;
+        }
+        ok = wait_or_abort(&bar_p, t & 1, abort_flag) && wait_or_abort(&full_c, (nc - 1) & 1, abort_flag);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
@@ -463,27 +450,6 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
   } else {
     const int row = tid;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    int no = 0;
-    if (has_state) {
-      const float w = decay_pow(ld, REV ? max((int64_t)0, end - 1 - (i0 + row)) : i0 + row - s0 + 1);
-      ok = warp_wait(&bar_o, no++ & 1, abort_flag);
-      if (ok) {
-        fence_after_sync();
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float v[32];
-          uint32_t u[32];
-          tmem_ld32(tm_o + lanes + c, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * w);
-          tmem_st32(tm_o + lanes + c, u);
-        }
-        tmem_wait_st();
-        fence_before_sync();
-        mbar_arrive(&bar_p);
-      }
-    }
     uint64_t col[16];   // lam^(31-cc), or lam^cc in the reverse direction, in pairs
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -537,12 +503,28 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
           *reinterpret_cast<uint4*>(cs + image_off(TM, i / (D / 8), i % (D / 8))) = make_uint4(0, 0, 0, 0);
         fence_proxy_async();
       }
+      if (t == 0 && has_state) {   // O = a X, row by row lam^e(i) of it, before the tiles are added
+        const float w = decay_pow(ld, REV ? max((int64_t)0, end - 1 - (i0 + row)) : i0 + row - s0 + 1);
+        ok = ok && warp_wait(&bar_o, 0, abort_flag);
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          uint32_t u[32];
+          tmem_ld32(tm_o + lanes + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * w);
+          tmem_st32(tm_o + lanes + c, u);
+        }
+      }
       tmem_wait_st();
       fence_before_sync();
       mbar_arrive(&bar_p);
     }
     // O of the last tile: to bf16 in a's buffer, then out
-    if (ok) ok = warp_wait(&bar_o, (no + n_tiles - 1) & 1, abort_flag);
+    if (ok) ok = warp_wait(&bar_o, (has_state + n_tiles - 1) & 1, abort_flag);
     if (ok) {
       fence_after_sync();
       const bool live = i0 + row < len;
