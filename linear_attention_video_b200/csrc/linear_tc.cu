@@ -53,17 +53,25 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("{\n\t.reg .b64 m;\n\tmov.b64 m, 0xbf800000bf800000;\n\tfma.rn.f32x2 %0, %2, m, %1;\n\t}" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// A bf16 pair as two fp32.
+__device__ __forceinline__ uint64_t wide2(uint32_t v) {
+  return pair2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
 __device__ __forceinline__ uint32_t pack2(uint64_t ab) {
   float a, b;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
   return pack2(a, b);
 }
-// a, b = bf16 pair + the rest
-__device__ __forceinline__ uint32_t take2(float& a, float& b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  a -= __low2float(v);
-  b -= __high2float(v);
-  return reinterpret_cast<const uint32_t&>(v);
+// ab = bf16 pair + the rest
+__device__ __forceinline__ uint32_t take2(uint64_t& ab) {
+  const uint32_t v = pack2(ab);
+  ab = sub2(ab, wide2(v));
+  return v;
 }
 // Bounded wait; a wait that gives up sets the CTA's flag, and every later wait returns at once.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -171,7 +179,13 @@ __global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __
     const int c8 = tid % 16, r0 = tid / 16;   // this thread's 8 channels, its tokens r0 + 16 i
     const int h = D == 128 ? h0 : min(h0 + c8 / 8, a.H - 1);
     const float ld = a.log_decay[h];
+    // the weight of a token of a whole tile: its row's power times the tile's, both at most 1
+    float roww[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) roww[i] = decay_pow(ld, a.reverse ? r0 + 16 * i + 1 : TL - 1 - r0 - 16 * i);
     for (int t = 0; ok && t < n_tiles; ++t) {
+      const int left = n_tok - t * TL;   // tokens from this tile on
+      const float tilew = decay_pow(ld, a.reverse ? t * TL : max(0, left - TL));
       ok = warp_wait(&full[t & 1], (t >> 1) & 1, abort_flag);
       if (ok && t > 0) ok = warp_wait(&done, (t - 1) & 1, abort_flag);   // mid and lo free
       if (!ok) break;
@@ -179,22 +193,21 @@ __global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __
       uint8_t* y = x + 16384;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 16 * i, tok = t * TL + r;
+        const int r = r0 + 16 * i;
         const uint32_t off = image_off(TL, r, c8);
         uint4 hi, m, l;
-        if (tok < n_tok) {
-          const float w = decay_pow(ld, a.reverse ? tok + 1 : n_tok - 1 - tok);
+        if (r < left) {
+          const float w = !a.reverse && left < TL ? decay_pow(ld, left - 1 - r) : roww[i] * tilew;
+          const uint64_t ww = pair2(w, w);
           const uint4 u = *reinterpret_cast<const uint4*>(y + off);
-          const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&u);
+          const uint32_t e[4] = {u.x, u.y, u.z, u.w};
           uint32_t *ph = &hi.x, *pm = &m.x, *pl = &l.x;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float2 f = __bfloat1622float2(e[j]);
-            f.x *= w;
-            f.y *= w;
-            ph[j] = take2(f.x, f.y);
-            pm[j] = take2(f.x, f.y);
-            pl[j] = pack2(f.x, f.y);
+            uint64_t f = mul2(wide2(e[j]), ww);
+            ph[j] = take2(f);
+            pm[j] = take2(f);
+            pl[j] = pack2(f);
           }
         } else {   // behind the end, whatever stands there
           hi = m = l = make_uint4(0, 0, 0, 0);
@@ -210,33 +223,42 @@ __global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __
     if (ok && n_tiles) ok = warp_wait(&done, (n_tiles - 1) & 1, abort_flag);
     if (ok) {
       fence_after_sync();
-      // lane = row of the 128 x 128 block; head = row / D owns columns of the same block
+      // lane = row of the 128 x 128 block; head = row / D owns columns of the same block.  The heads' images are put
+      // together over the x and y stages and leave as whole.
       const int row = (warp & 3) * 32 + (tid & 31), hp = row / D, r = row % D;
       constexpr int COLS = D / 2;   // columns of this warp: a half of its head's
-      const int c0 = hp * D % 128 + (warp >> 2) * COLS;
-      const bool live = h0 + hp < a.H;
-      uint8_t* img = reinterpret_cast<uint8_t*>(a.local) + ((((int64_t)b * a.H + h0 + hp) * a.n_seg + seg) * D * D) * 4;
-#pragma unroll
+      const int c0 = (warp >> 2) * COLS;
+      const uint32_t at = tm + ((uint32_t)((warp & 3) * 32) << 16) + hp * (D % 128) + c0;
+      uint8_t* img = sm + hp * D * D * 4;
+#pragma unroll 1
       for (int c = 0; c < COLS; c += 16) {
         float v[16], w[16];
         if (n_tiles) {
-          tmem_ld16(tm + ((uint32_t)((warp & 3) * 32) << 16) + c0 + c, v);
-          tmem_ld16(tm + ((uint32_t)((warp & 3) * 32) << 16) + 128 + c0 + c, w);
+          tmem_ld16(at + c, v);
+          tmem_ld16(at + 128 + c, w);
           tmem_wait_ld();
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = w[i] = 0.f;
         }
-        if (live) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 8) {
-            const uint32_t off = image_off(D, r, (c0 - hp * D % 128 + c + i) / 8);
-            *reinterpret_cast<float4*>(img + off) = make_float4(v[i] + w[i], v[i + 1] + w[i + 1], v[i + 2] + w[i + 2], v[i + 3] + w[i + 3]);
-            *reinterpret_cast<float4*>(img + D * D * 2 + off) =
-                make_float4(v[i + 4] + w[i + 4], v[i + 5] + w[i + 5], v[i + 6] + w[i + 6], v[i + 7] + w[i + 7]);
-          }
+        for (int i = 0; i < 16; i += 8) {
+          const uint32_t off = image_off(D, r, (c0 + c + i) / 8);
+          *reinterpret_cast<float4*>(img + off) = make_float4(v[i] + w[i], v[i + 1] + w[i + 1], v[i + 2] + w[i + 2], v[i + 3] + w[i + 3]);
+          *reinterpret_cast<float4*>(img + D * D * 2 + off) =
+              make_float4(v[i + 4] + w[i + 4], v[i + 5] + w[i + 5], v[i + 6] + w[i + 6], v[i + 7] + w[i + 7]);
         }
       }
+      fence_proxy_async();
+    }
+    ok = named_sync_and(1, 256, ok);
+    if (ok && tid == 0) {
+#pragma unroll
+      for (int p = 0; p < HP; ++p)
+        if (h0 + p < a.H)
+          bulk_s2g(a.local + (((int64_t)b * a.H + h0 + p) * a.n_seg + seg) * D * D, sm + p * D * D * 4, D * D * 4);
+      bulk_commit();
+      bulk_wait_read();
     }
   }
   fence_before_sync();
