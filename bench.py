@@ -502,7 +502,8 @@ def ours_arm(args, w, idx, rank, world, local_rank):
 
 def mixer_arm(args, rank, world, local_rank):
     """KDA/MLA 3:1 against MHA/MLA 3:1 token-mixer stacks as N grows (synthetic weights, one GPU
-    per rank, every rank the same sweep): forward latency and peak memory per stack."""
+    per rank, every rank the same sweep): forward latency and peak memory per stack; the linear/MLA
+    3:1 stack (one decay per head instead of KDA's gates and delta rule) beside them."""
     import torch
     from linear_attention_video_b200 import mixer
     dev = torch.device("cuda", local_rank)
@@ -515,7 +516,7 @@ def mixer_arm(args, rank, world, local_rank):
         for T in frames:
             N = text_len + T * Hg * Wg
             row = {"frames": T, "tokens": N}
-            for kind in ("kda", "mha"):
+            for kind in ("kda", "mha", "linear"):
                 torch.cuda.empty_cache()
                 torch.cuda.reset_peak_memory_stats(dev)
                 try:

@@ -156,7 +156,7 @@ cudaError_t launch_linear_bwd(const Dims& d, kda_dtype dt, const void* q, const 
                               const float* dSN, void* dq, void* dk, void* dv, float* dS0, void* scratch,
                               uint32_t* status, cudaStream_t s, int* launches);
 // bf16 problems (linear_tc.cu); the states between the launches are hi and lo images (see there).
-int linear_tc_segment();
+int linear_tc_segment(const Dims& d);
 cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s);
 cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanArgs& a, bool local, cudaStream_t s);
 cudaError_t launch_linear_tc_map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s);

@@ -451,7 +451,7 @@ struct Pass {
   int* launches;
 
   Pass(const Dims& d_, kda_dtype dt, const float* ld, const int32_t* len, uint32_t* st, cudaStream_t s_, int* l)
-      : d(d_), tc(dt == KDA_DT_BF16), seg(tc ? linear_tc_segment() : kSeg),
+      : d(d_), tc(dt == KDA_DT_BF16), seg(tc ? linear_tc_segment(d_) : kSeg),
         n_seg((int)((d_.N + seg - 1) / seg)), log_decay(ld), lengths(len), status(st), s(s_), launches(l) {}
 
   size_t state_floats() const { return (size_t)d.B * d.H * n_seg * d.dk * d.dv; }

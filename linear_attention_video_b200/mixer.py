@@ -2,10 +2,11 @@
 KDA/MLA 3:1 stack against an MHA/MLA 3:1 stack as the token count grows (paper.rainbus.top,
 实验结果 and Figure 18; genai-atlas, "Evidence": the hybrid runs 2.14x faster at 255k tokens).
 
-Only the KDA layer's short conv and scan are this library's kernels (``kda_fwd``); the linear
-projections are bf16 cuBLAS GEMMs (torch.matmul), the gate activations are torch element-wise ops,
-and the softmax attention of the MHA and MLA layers is PyTorch's fused scaled-dot-product attention
-(a library kernel, like cuBLAS), bidirectional over all tokens.
+The KDA layer's short conv and scan are this library's kernels (``kda_fwd``), and so are the norm, the
+rotary positions and the linear attention of the linear layer; the linear projections are bf16 cuBLAS
+GEMMs (torch.matmul), the gate activations are torch element-wise ops, and the softmax attention of the
+MHA and MLA layers is PyTorch's fused scaled-dot-product attention (a library kernel, like cuBLAS),
+bidirectional over all tokens.
 
 Layer readings (the pages give no sizes for the MLA projections):
   * width D = H * d (16 heads of 128: width 2048, the largest trained model's);
@@ -15,7 +16,12 @@ Layer readings (the pages give no sizes for the MLA projections):
   * MHA: q, k, v of 128 per head, softmax scale 1/sqrt(128);
   * KDA: q, k, v projections (q and k scaled to a norm of about 1 per head), log alpha =
     -softplus(x Wa - 5) per channel (alpha near 0.99), beta = sigmoid(x Wb) per head, the
-    modality-aware short conv and the scan (no scale on q), output projection.
+    modality-aware short conv and the scan (no scale on q), output projection;
+  * linear (no counterpart in the pages; the mixer with the coarsest memory, one constant decay per
+    head, to compare the KDA layer's gates against): layer norm of the input, q, k, v projections,
+    rotary positions over (t, h, w) on q and k, linear attention with a decay per head, output
+    projection.  It trains (``backward``), takes prompts of different lengths in one padded batch, and
+    goes on token by token (``step``).
 """
 from __future__ import annotations
 
@@ -24,10 +30,13 @@ import math
 import torch
 import torch.nn.functional as F
 
-from . import alloc_workspace, kda_fwd, problem
+from . import (alloc_layernorm_bwd_workspace, alloc_linear_bwd_workspace, alloc_linear_workspace, alloc_workspace,
+               kda_fwd, kda_layernorm_bwd, kda_layernorm_fwd, kda_linear_bwd, kda_linear_fwd, kda_linear_step,
+               kda_rope_bwd, kda_rope_fwd, problem, rope)
 
 D_LATENT, D_NOPE, D_DIRECT = 512, 96, 32
 GATE_BIAS = -5.0   # log alpha = -softplus(x Wa - 5): alpha near 0.99, the long-memory regime
+ROPE_BASE = 10000.0
 
 
 def _w(g, shape, fan_in, device, scale=1.0):
@@ -124,12 +133,94 @@ class KDALayer:
         return self.mix(x).view(B, N, -1) @ self.wo
 
 
+class LinearLayer:
+    """Layer norm, projections, rotary positions, linear attention with a constant decay per head, output
+    projection.  Sized for one token layout (text_len + T * Hg * Wg tokens); ``step`` takes any position."""
+
+    def __init__(self, B, H, d, text_len, grid, device="cuda", seed=3, workspace=None):
+        g = torch.Generator().manual_seed(seed)
+        D = H * d
+        self.B, self.H, self.d = B, H, d
+        # q of norm about 1 and k of about sqrt(d): scores q . k of about 1
+        self.wq = _w(g, (D, D), D, device, 1.0 / math.sqrt(d))
+        self.wk, self.wv, self.wo = (_w(g, (D, D), D, device) for _ in range(3))
+        self.norm_w = (1.0 + 0.1 * torch.randn(D, generator=g)).to(device)
+        self.norm_b = (0.1 * torch.randn(D, generator=g)).to(device)
+        # heads that forget from within two tokens to over some hundreds
+        self.log_decay = torch.tensor([-(2.0 ** (-8.0 * (h + 1) / H)) for h in range(H)], device=device)
+        # a quarter of a head's pairs follow time, the rest height and width; a ladder of frequencies per axis
+        n_t = d // 8
+        pairs = (n_t, (d // 2 - n_t) // 2, d // 2 - n_t - (d // 2 - n_t) // 2)
+        self.rope = rope(pairs)
+        self.inv_freq = torch.cat([ROPE_BASE ** (-torch.arange(n, dtype=torch.float64) / n) for n in pairs]).float().to(device)
+        self.p = problem(B, H, d, text_len, grid)
+        self.p1 = problem(B, H, d, 1, (0, 0, 0))
+        self.ws = alloc_linear_workspace(self.p, torch.bfloat16, device) if workspace is None else workspace
+        self.ws_bwd = None
+
+    def _qkv(self, p, x, positions, stats=None):
+        """The normalised input and q, k (turned), v, each [B, N, H, d]."""
+        B, N, D = x.shape
+        h = torch.empty_like(x)
+        kda_layernorm_fwd(x, h, self.norm_w, self.norm_b, 1e-5, *(stats or (None, None)))
+        q, k, v = ((h @ w).view(B, N, self.H, self.d) for w in (self.wq, self.wk, self.wv))
+        kda_rope_fwd(p, self.rope, q, k, self.inv_freq, q, k, positions=positions)
+        return h, q, k, v
+
+    def mix(self, x, lengths=None, initial_state=None, final_state=None, positions=None):
+        """The attention output [B, N, H, d] (bf16), before the output projection."""
+        _, q, k, v = self._qkv(self.p, x, positions)
+        o = torch.empty_like(v)
+        kda_linear_fwd(self.p, q, k, v, self.log_decay, o, self.ws, lengths=lengths, initial_state=initial_state,
+                       final_state=final_state)
+        return o
+
+    def __call__(self, x, **kw):
+        B, N, _ = x.shape
+        return self.mix(x, **kw).view(B, N, -1) @ self.wo
+
+    def step(self, x, state, positions):
+        """One token per item: x [B, 1, D], positions [B, 1, 3] int32; advances state [B, H, d, d] in place."""
+        _, q, k, v = self._qkv(self.p1, x, positions)
+        o = torch.empty_like(v)
+        kda_linear_step(self.p1, q, k, v, self.log_decay, state, o, state)
+        return o.view(self.B, 1, -1) @ self.wo
+
+    def backward(self, x, dy, lengths=None, positions=None):
+        """Gradients of sum(dy * self(x)): that of x, and a dict of the weights'.  The forward pass up to the
+        attention is computed again; nothing of it has to be kept."""
+        B, N, D = x.shape
+        rows = B * N
+        mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
+        h, q, k, v = self._qkv(self.p, x, positions, (mean, rstd))
+        o = torch.empty_like(v)
+        kda_linear_fwd(self.p, q, k, v, self.log_decay, o, self.ws, lengths=lengths)
+        if self.ws_bwd is None:
+            self.ws_bwd = (alloc_linear_bwd_workspace(self.p, x.dtype, x.device),
+                           alloc_layernorm_bwd_workspace(rows, D, x.device))
+        d_o = (dy @ self.wo.t()).view(B, N, self.H, self.d)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        kda_linear_bwd(self.p, q, k, v, self.log_decay, d_o, dq, dk, dv, self.ws_bwd[0], lengths=lengths)
+        kda_rope_bwd(self.p, self.rope, dq, dk, self.inv_freq, dq, dk, positions=positions)
+        flat = lambda t: t.reshape(rows, D)   # noqa: E731
+        grads = {"wo": flat(o).t() @ flat(dy), "wq": flat(h).t() @ flat(dq), "wk": flat(h).t() @ flat(dk),
+                 "wv": flat(h).t() @ flat(dv)}
+        dh = flat(dq) @ self.wq.t()
+        dh.addmm_(flat(dk), self.wk.t())
+        dh.addmm_(flat(dv), self.wv.t())
+        dx = torch.empty_like(x)
+        grads["norm_w"], grads["norm_b"] = torch.empty_like(self.norm_w), torch.empty_like(self.norm_b)
+        kda_layernorm_bwd(dh, x, mean, rstd, dx, self.ws_bwd[1], self.norm_w, grads["norm_w"], grads["norm_b"])
+        return dx, grads
+
+
 def stack(kind: str, B, H, d, text_len, grid, device="cuda"):
-    """Four token mixers: 'kda' = KDA, KDA, KDA, MLA; 'mha' = MHA, MHA, MHA, MLA (the pages' 3:1)."""
-    if kind == "kda":
-        first = KDALayer(B, H, d, text_len, grid, device, seed=10)
-        layers = [first] + [KDALayer(B, H, d, text_len, grid, device, seed=10 + i, workspace=first.ws)
-                            for i in (1, 2)]
+    """Four token mixers: 'kda' = KDA, KDA, KDA, MLA; 'mha' = MHA, MHA, MHA, MLA (the pages' 3:1); 'linear' =
+    linear, linear, linear, MLA."""
+    if kind in ("kda", "linear"):
+        layer = KDALayer if kind == "kda" else LinearLayer
+        first = layer(B, H, d, text_len, grid, device, seed=10)
+        layers = [first] + [layer(B, H, d, text_len, grid, device, seed=10 + i, workspace=first.ws) for i in (1, 2)]
     elif kind == "mha":
         layers = [MHALayer(H, d, device, seed=10 + i) for i in range(3)]
     else:
