@@ -160,6 +160,10 @@ int linear_tc_segment(const Dims& d);
 cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s);
 cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanArgs& a, bool local, cudaStream_t s);
 cudaError_t launch_linear_tc_map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s);
+// fp32 problems (linear_tc32.cu).
+int linear_tc32_segment();
+cudaError_t launch_linear_tc32_local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s);
+cudaError_t launch_linear_tc32_map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s);
 cudaError_t launch_linear_step(const Dims& d, kda_dtype dt, const LinStepArgs& a, cudaStream_t s, int* launches);
 
 // Host-side validation (kda_api.cu), returning a kda_status.
