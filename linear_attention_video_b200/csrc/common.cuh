@@ -116,7 +116,7 @@ struct LinLocalArgs {
   const int32_t* lengths;
   float* local;      // [B][H][n_seg][D][D]
   int64_t N;
-  int H, n_seg;
+  int H, n_seg, seg; // segments, and tokens of one
   bool reverse;      // weights towards the segment's first token instead of its last
 };
 struct LinScanArgs {
@@ -136,7 +136,7 @@ struct LinMapArgs {
   const float* log_decay;
   const int32_t* lengths;
   int64_t N;
-  int H, n_seg;
+  int H, n_seg, seg;
   bool reverse, transposed;
 };
 struct LinStepArgs {

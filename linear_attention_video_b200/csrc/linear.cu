@@ -158,7 +158,7 @@ struct Pass {
     if (!local && !last && !(bf16 && initial)) return cudaSuccess;   // nothing enters, or the initial state as it is
     cudaError_t e;
     if (local) {
-      const LinLocalArgs a{x, y, log_decay, lengths, out, d.N, d.H, n_seg, reverse};
+      const LinLocalArgs a{x, y, log_decay, lengths, out, d.N, d.H, n_seg, seg, reverse};
       if ((e = bf16 ? launch_linear_tc_local(d, a, status, s) : launch_linear_tc32_local(d, a, status, s)) != cudaSuccess) return e;
       *launches += 1;
     }
@@ -171,7 +171,7 @@ struct Pass {
   cudaError_t map(const void* a, const void* b, const void* c, void* out, const float* st, const float* initial,
                   bool reverse, bool transposed) {
     if (n_seg == 0) return cudaSuccess;
-    const LinMapArgs m{a, b, c, out, st, initial, log_decay, lengths, d.N, d.H, n_seg, reverse, transposed};
+    const LinMapArgs m{a, b, c, out, st, initial, log_decay, lengths, d.N, d.H, n_seg, seg, reverse, transposed};
     const cudaError_t e = bf16 ? launch_linear_tc_map(d, m, status, s) : launch_linear_tc32_map(d, m, status, s);
     if (e == cudaSuccess) *launches += 1;
     return e;

@@ -24,10 +24,7 @@ namespace {
 
 using namespace tc;
 
-// Tokens per segment: a longer one costs the map more tiles of scores per row, a shorter one costs states.  189,272
-// tokens x 16 x 128: 256 1.38 ms, 512 1.32, 1024 1.52; 4 x 8192 x 16 x 64, whose states are a quarter as large: 256
-// 145 us, 512 159, 1024 209.
-template <int D> constexpr int kSeg = D == 128 ? 512 : 256;
+constexpr int kMaxSeg = 512;   // tokens per segment, at most; always a multiple of TM
 constexpr int TM = 128;       // tokens per tile of the map
 constexpr int TL = 64;        // tokens per tile of the local sums
 
@@ -58,7 +55,7 @@ __global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __
   const int tid = threadIdx.x, warp = tid / 32;
   constexpr int HP = 128 / D;   // heads per CTA
   const int seg = blockIdx.x, h0 = blockIdx.y * HP, b = blockIdx.z;
-  const int64_t s0 = (int64_t)seg * kSeg<D>, len = item_tokens(a.lengths, b, a.N), end = min(len, s0 + kSeg<D>);
+  const int64_t s0 = (int64_t)seg * a.seg, len = item_tokens(a.lengths, b, a.N), end = min(len, s0 + a.seg);
   const int n_tok = (int)max((int64_t)0, end - s0), n_tiles = (n_tok + TL - 1) / TL;
   if (tid == 0) {
     mbar_init(&full[0], 1);
@@ -286,7 +283,7 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_slot;
   __shared__ float diag[64];                // lam^n at 32 + n, zeros below
-  __shared__ float power32[4 * kSeg<D> / TM];   // lam^(32 n)
+  __shared__ float power32[4 * kMaxSeg / TM];   // lam^(32 n)
   uint8_t* as = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   uint8_t* bs = as + L::tile;
   uint8_t* cs = bs + L::tile;
@@ -294,8 +291,8 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t i0 = (int64_t)blockIdx.x * TM, len = item_tokens(a.lengths, b, a.N);
-  const int seg = (int)(i0 / kSeg<D>);
-  const int64_t s0 = (int64_t)seg * kSeg<D>, end = min(len, s0 + kSeg<D>);
+  const int seg = (int)(i0 / a.seg);
+  const int64_t s0 = (int64_t)seg * a.seg, end = min(len, s0 + a.seg);
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)b * a.N * a.H + h) * D;
   if (i0 >= len) {   // behind the item's end: zeros
     const int n = (int)min((int64_t)TM, a.N - i0) * (D / 8);
@@ -318,7 +315,7 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
     fence_mbar_init();
   }
   if (tid < 64) diag[tid] = tid < 32 ? 0.f : decay_pow(ld, tid - 32);
-  else if (tid < 64 + 4 * kSeg<D> / TM) power32[tid - 64] = decay_pow(ld, 32 * (tid - 64));
+  else if (tid < 64 + 4 * kMaxSeg / TM) power32[tid - 64] = decay_pow(ld, 32 * (tid - 64));
   if (warp == 4) { tmem_alloc(&tmem_slot, 256); tmem_relinquish(); }
   fence_before_sync();
   __syncthreads();
@@ -407,7 +404,7 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
       col[i] = REV ? pair2(diag[32 + 2 * i], diag[33 + 2 * i]) : pair2(diag[63 - 2 * i], diag[62 - 2 * i]);
     // a row's distance to the nearest column of an earlier (later) group is rowf's plus a multiple of 32
     const float rowf = decay_pow(ld, REV ? 32 - lane : lane + 1);
-    const int to_end = (int)min((int64_t)kSeg<D>, len - j_first);   // tokens of the sequence from j_first on
+    const int to_end = (int)min((int64_t)a.seg, len - j_first);   // tokens of the sequence from j_first on
     for (int t = 0; ok && t < n_tiles; ++t) {
       ok = warp_wait(&bar_s, t & 1, abort_flag);
       if (!ok) break;
@@ -551,7 +548,15 @@ cudaError_t map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream
 
 }  // namespace
 
-int linear_tc_segment(const Dims& d) { return d.dk == 128 ? kSeg<128> : kSeg<64>; }
+// Tokens per segment.  A longer one costs the map more tiles of scores per row, a shorter one costs states: 189,272
+// tokens x 16 x 128 take 1.38 ms with 256, 1.32 with 512 and 1.52 with 1024; 4 x 8192 x 16 x 64, whose states are a
+// quarter as large, 145 us with 256 and 159 with 512.  Where the segments would not give every SM its two CTAs of the
+// local sums, shorter ones take less time in a row.
+int linear_tc_segment(const Dims& d) {
+  int seg = d.dk == 128 ? kMaxSeg : kMaxSeg / 2;
+  while (seg > TM && (int64_t)d.B * d.H * ((d.N + seg - 1) / seg) < 2 * 148) seg /= 2;
+  return seg;
+}
 
 cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s) {
   return d.dk == 128 ? local<128>(d, a, status, s) : local<64>(d, a, status, s);
