@@ -119,6 +119,9 @@ struct LinLocalArgs {
   int H, n_seg, seg; // segments, and tokens of one
   bool reverse;      // weights towards the segment's first token instead of its last
 };
+// A launch does the work of up to two or three such sets side by side (the backward pass's states and gradients, and
+// its three maps): grid.x is a multiple of one set's.
+struct LinLocalSets { LinLocalArgs set[2]; int n; };
 struct LinScanArgs {
   float* states;           // [B][H][n_seg][D][D], in place
   const float* initial;    // [B][H][D][D] or NULL (zero)
@@ -128,7 +131,9 @@ struct LinScanArgs {
   int64_t N, dd;
   int seg, H, n_seg;
   bool reverse;
+  bool local;              // states holds local contributions; otherwise nothing but `initial` enters
 };
+struct LinScanSets { LinScanArgs set[2]; int n; };
 struct LinMapArgs {
   const void *a, *b, *c;
   void* out;
@@ -139,6 +144,7 @@ struct LinMapArgs {
   int H, n_seg, seg;
   bool reverse, transposed;
 };
+struct LinMapSets { LinMapArgs set[3]; int n; };
 struct LinStepArgs {
   const void *q, *k, *v;
   const float *log_decay, *state_in;
@@ -155,15 +161,15 @@ cudaError_t launch_linear_bwd(const Dims& d, kda_dtype dt, const void* q, const 
                               const float* log_decay, const int32_t* lengths, const float* S0, const void* d_o,
                               const float* dSN, void* dq, void* dk, void* dv, float* dS0, void* scratch,
                               uint32_t* status, cudaStream_t s, int* launches);
-// bf16 problems (linear_tc.cu); the states between the launches are hi and lo images (see there).
+// bf16 problems (linear_tc.cu); the states between the launches are operand images (see there).
 int linear_tc_segment(const Dims& d);
-cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s);
-cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanArgs& a, bool local, cudaStream_t s);
-cudaError_t launch_linear_tc_map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s);
+cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalSets& a, uint32_t* status, cudaStream_t s);
+cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanSets& a, cudaStream_t s);
+cudaError_t launch_linear_tc_map(const Dims& d, const LinMapSets& a, uint32_t* status, cudaStream_t s);
 // fp32 problems (linear_tc32.cu).
 int linear_tc32_segment();
-cudaError_t launch_linear_tc32_local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s);
-cudaError_t launch_linear_tc32_map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s);
+cudaError_t launch_linear_tc32_local(const Dims& d, const LinLocalSets& a, uint32_t* status, cudaStream_t s);
+cudaError_t launch_linear_tc32_map(const Dims& d, const LinMapSets& a, uint32_t* status, cudaStream_t s);
 cudaError_t launch_linear_step(const Dims& d, kda_dtype dt, const LinStepArgs& a, cudaStream_t s, int* launches);
 
 // Host-side validation (kda_api.cu), returning a kda_status.

@@ -14,6 +14,7 @@
 //
 // The local sums and the map run on the tensor cores, in linear_tc.cu for bf16 problems and linear_tc32.cu for fp32
 // ones; here are the recurrence of fp32 problems, the single token and the passes over a problem.
+#include <initializer_list>
 #include <type_traits>
 
 #include "linear_tc.cuh"
@@ -36,9 +37,12 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
 // ---------------------------------------------------------------------------
 // recurrence over segments, in place: local contributions become what enters each segment
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(128) lin_scan_kernel(LinScanArgs a) {
+template <bool ONE>
+__global__ void __launch_bounds__(128) lin_scan_kernel(const __grid_constant__ LinScanSets sets) {
+  const int per_set = ONE ? gridDim.x : gridDim.x / sets.n, which = ONE ? 0 : blockIdx.x / per_set;
+  const LinScanArgs& a = sets.set[which];
   const int bh = blockIdx.y, h = bh % a.H, b = bh / a.H;
-  const int64_t e = ((int64_t)blockIdx.x * 128 + threadIdx.x) * 4;   // element of the D x D state
+  const int64_t e = ((int64_t)(blockIdx.x - which * per_set) * 128 + threadIdx.x) * 4;   // element of the D x D state
   const int64_t dd = a.dd, len = item_tokens(a.lengths, b, a.N);
   const float ld = a.log_decay[h];
   const int64_t last = len / a.seg;   // the segment that holds the end, if it is not whole
@@ -131,10 +135,20 @@ template <typename F> cudaError_t dispatch(const Dims& d, kda_dtype dt, F f) {
   return d.dk == 128 ? f(float(), integral_constant<int, 128>()) : f(float(), integral_constant<int, 64>());
 }
 
-cudaError_t launch_scan(const Dims& d, const LinScanArgs& a, cudaStream_t s) {
-  lin_scan_kernel<<<dim3((unsigned)(a.dd / 512), d.B * d.H), 128, 0, s>>>(a);
+cudaError_t launch_scan(const Dims& d, const LinScanSets& a, cudaStream_t s) {
+  const auto kernel = a.n == 1 ? lin_scan_kernel<true> : lin_scan_kernel<false>;
+  kernel<<<dim3((unsigned)(a.set[0].dd / 512 * a.n), d.B * d.H), 128, 0, s>>>(a);
   return cudaGetLastError();
 }
+
+// Of the states in one direction: the sums w x y^T, what they start from, and where they go.
+struct States {
+  const void *x, *y;
+  float* out;             // what enters every segment
+  const float* initial;
+  float* last;            // what leaves the last one, or NULL
+  bool reverse;
+};
 // What a pass over one problem needs to know: its kernels' segment length, and the three launches.
 struct Pass {
   const Dims& d;
@@ -152,26 +166,33 @@ struct Pass {
 
   size_t state_floats() const { return (size_t)d.B * d.H * n_seg * d.dk * d.dv; }
 
-  // What enters every segment (in the direction of the pass) of sum w x y^T; `last`: what leaves the last one.
-  cudaError_t states(const void* x, const void* y, float* out, const float* initial, float* last, bool reverse) {
-    const bool local = n_seg > 1 || (n_seg == 1 && last);
-    if (!local && !last && !(bf16 && initial)) return cudaSuccess;   // nothing enters, or the initial state as it is
+  cudaError_t states(std::initializer_list<States> all) {
+    LinLocalSets l = {};
+    LinScanSets c = {};
+    for (const States& w : all) {
+      const bool local = n_seg > 1 || (n_seg == 1 && w.last);
+      if (!local && !w.last && !(bf16 && w.initial)) continue;   // nothing enters, or the initial state as it is
+      if (local) l.set[l.n++] = {w.x, w.y, log_decay, lengths, w.out, d.N, d.H, n_seg, seg, w.reverse};
+      c.set[c.n++] = {w.out, w.initial, w.last, log_decay, lengths, d.N, (int64_t)d.dk * d.dv, seg, d.H, n_seg, w.reverse, local};
+    }
     cudaError_t e;
-    if (local) {
-      const LinLocalArgs a{x, y, log_decay, lengths, out, d.N, d.H, n_seg, seg, reverse};
-      if ((e = bf16 ? launch_linear_tc_local(d, a, status, s) : launch_linear_tc32_local(d, a, status, s)) != cudaSuccess) return e;
+    if (l.n) {
+      if ((e = bf16 ? launch_linear_tc_local(d, l, status, s) : launch_linear_tc32_local(d, l, status, s)) != cudaSuccess) return e;
       *launches += 1;
     }
-    const LinScanArgs a{out, initial, last, log_decay, lengths, d.N, (int64_t)d.dk * d.dv, seg, d.H, n_seg, reverse};
-    if ((e = bf16 ? launch_linear_tc_scan(d, a, local, s) : launch_scan(d, a, s)) != cudaSuccess) return e;
-    *launches += 1;
+    if (c.n) {
+      if ((e = bf16 ? launch_linear_tc_scan(d, c, s) : launch_scan(d, c, s)) != cudaSuccess) return e;
+      *launches += 1;
+    }
     return cudaSuccess;
   }
 
-  cudaError_t map(const void* a, const void* b, const void* c, void* out, const float* st, const float* initial,
-                  bool reverse, bool transposed) {
+  LinMapArgs one(const void* a, const void* b, const void* c, void* out, const float* st, const float* initial,
+                 bool reverse, bool transposed) const {
+    return {a, b, c, out, st, initial, log_decay, lengths, d.N, d.H, n_seg, seg, reverse, transposed};
+  }
+  cudaError_t map(const LinMapSets& m) {
     if (n_seg == 0) return cudaSuccess;
-    const LinMapArgs m{a, b, c, out, st, initial, log_decay, lengths, d.N, d.H, n_seg, seg, reverse, transposed};
     const cudaError_t e = bf16 ? launch_linear_tc_map(d, m, status, s) : launch_linear_tc32_map(d, m, status, s);
     if (e == cudaSuccess) *launches += 1;
     return e;
@@ -193,8 +214,8 @@ cudaError_t launch_linear_fwd(const Dims& d, kda_dtype dt, const void* q, const 
   Pass p(d, dt, log_decay, lengths, status, s, launches);
   float* states = static_cast<float*>(scratch);
   cudaError_t e;
-  if ((e = p.states(k, v, states, S0, SN, false)) != cudaSuccess) return e;
-  return p.map(q, k, v, o, states, S0, false, false);
+  if ((e = p.states({{k, v, states, S0, SN, false}})) != cudaSuccess) return e;
+  return p.map({{p.one(q, k, v, o, states, S0, false, false)}, 1});
 }
 
 cudaError_t launch_linear_bwd(const Dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
@@ -205,11 +226,9 @@ cudaError_t launch_linear_bwd(const Dims& d, kda_dtype dt, const void* q, const 
   float* states = static_cast<float*>(scratch);
   float* grads = states + p.state_floats();
   cudaError_t e;
-  if ((e = p.states(k, v, states, S0, nullptr, false)) != cudaSuccess) return e;
-  if ((e = p.states(q, d_o, grads, dSN, dS0, true)) != cudaSuccess) return e;
-  if ((e = p.map(d_o, v, k, dq, states, S0, false, true)) != cudaSuccess) return e;
-  if ((e = p.map(v, d_o, q, dk, grads, dSN, true, true)) != cudaSuccess) return e;
-  return p.map(k, q, d_o, dv, grads, dSN, true, false);
+  if ((e = p.states({{k, v, states, S0, nullptr, false}, {q, d_o, grads, dSN, dS0, true}})) != cudaSuccess) return e;
+  return p.map({{p.one(d_o, v, k, dq, states, S0, false, true), p.one(v, d_o, q, dk, grads, dSN, true, true),
+                 p.one(k, q, d_o, dv, grads, dSN, true, false)}, 3});
 }
 
 cudaError_t launch_linear_step(const Dims& d, kda_dtype dt, const LinStepArgs& a, cudaStream_t s, int* launches) {

@@ -40,10 +40,12 @@ constexpr int kLocalThreads = 288;
 constexpr int kLocalSmem = 1024 + 2 * 32768 + 32768;
 
 struct LocalMaps { CUtensorMap x, y; };
+struct LocalMapSets { LocalMaps set[2]; };
 
-template <int D>
-__global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __grid_constant__ LocalMaps maps,
-                                                                       LinLocalArgs a, uint32_t* status) {
+template <int D, bool ONE>
+__global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __grid_constant__ LocalMapSets map_sets,
+                                                                       const __grid_constant__ LinLocalSets sets,
+                                                                       uint32_t* status) {
   extern __shared__ uint8_t dyn[];
   __shared__ uint64_t full[2], ready, done;
   __shared__ uint32_t tmem_slot;
@@ -54,7 +56,10 @@ __global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __
   volatile int* abort_flag = &abort_slot;
   const int tid = threadIdx.x, warp = tid / 32;
   constexpr int HP = 128 / D;   // heads per CTA
-  const int seg = blockIdx.x, h0 = blockIdx.y * HP, b = blockIdx.z;
+  const int per_set = ONE ? gridDim.x : gridDim.x / sets.n, which = ONE ? 0 : blockIdx.x / per_set;
+  const LocalMaps& maps = map_sets.set[which];
+  const LinLocalArgs& a = sets.set[which];
+  const int seg = blockIdx.x - which * per_set, h0 = blockIdx.y * HP, b = blockIdx.z;
   const int64_t s0 = (int64_t)seg * a.seg, len = item_tokens(a.lengths, b, a.N), end = min(len, s0 + a.seg);
   const int n_tok = (int)max((int64_t)0, end - s0), n_tiles = (n_tok + TL - 1) / TL;
   if (tid == 0) {
@@ -207,11 +212,13 @@ __global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __
 // scan
 // ---------------------------------------------------------------------------
 // A thread takes 8 columns of one row: 32 bytes of the local state, 16 of the image over them.
-// local = false: nothing but the initial state enters (one segment, no final state wanted).
-template <int D>
-__global__ void __launch_bounds__(128) lin_tc_scan_kernel(LinScanArgs a, bool local) {
+template <int D, bool ONE>
+__global__ void __launch_bounds__(128) lin_tc_scan_kernel(const __grid_constant__ LinScanSets sets) {
+  constexpr int kPerSet = D * D / 8 / 128;
+  const LinScanArgs& a = sets.set[ONE ? 0 : blockIdx.x / kPerSet];
+  const bool local = a.local;
   const int bh = blockIdx.y, h = bh % a.H, b = bh / a.H;
-  const int e = blockIdx.x * 128 + threadIdx.x, r = e / (D / 8), c8 = e % (D / 8);
+  const int e = blockIdx.x % kPerSet * 128 + threadIdx.x, r = e / (D / 8), c8 = e % (D / 8);
   const int64_t len = item_tokens(a.lengths, b, a.N), last = len / a.seg;
   const float ld = a.log_decay[h];
   const Factor whole = segment_factor(ld, a.seg), part = segment_factor(ld, len % a.seg);
@@ -272,11 +279,11 @@ template <int D> struct MapSmem {
 };
 
 struct MapMaps { CUtensorMap a, b, c, out; };
+struct MapMapSets { MapMaps set[3]; };
 
 // P of one group of 32 columns: s * factor(row, group) * col[cc], or on the diagonal block s * lam^|i-j|.
 template <int D, bool REV>
-__global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid_constant__ MapMaps maps, LinMapArgs a,
-                                                                   uint32_t* status) {
+__device__ __forceinline__ void map_tile(const MapMaps& maps, const LinMapArgs& a, int tile, uint32_t* status) {
   using L = MapSmem<D>;
   extern __shared__ uint8_t dyn[];
   __shared__ uint64_t bar_a, full_b, full_c, bar_s, bar_o, bar_p;
@@ -290,7 +297,7 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
   volatile int* abort_flag = &abort_slot;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int h = blockIdx.y, b = blockIdx.z;
-  const int64_t i0 = (int64_t)blockIdx.x * TM, len = item_tokens(a.lengths, b, a.N);
+  const int64_t i0 = (int64_t)tile * TM, len = item_tokens(a.lengths, b, a.N);
   const int seg = (int)(i0 / a.seg);
   const int64_t s0 = (int64_t)seg * a.seg, end = min(len, s0 + a.seg);
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)b * a.N * a.H + h) * D;
@@ -509,6 +516,19 @@ __global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid
   if (warp == 4) tmem_dealloc(tm_s, 256);
 }
 
+// ONE: the forward pass's map alone; otherwise the backward pass's three.
+template <int D, bool ONE>
+__global__ void __launch_bounds__(kMapThreads, 2) lin_tc_map_kernel(const __grid_constant__ MapMapSets map_sets,
+                                                                   const __grid_constant__ LinMapSets sets, uint32_t* status) {
+  if constexpr (ONE) {
+    map_tile<D, false>(map_sets.set[0], sets.set[0], blockIdx.x, status);
+  } else {
+    const int per_set = gridDim.x / sets.n, which = blockIdx.x / per_set, tile = blockIdx.x % per_set;
+    if (sets.set[which].reverse) map_tile<D, true>(map_sets.set[which], sets.set[which], tile, status);
+    else map_tile<D, false>(map_sets.set[which], sets.set[which], tile, status);
+  }
+}
+
 // [B][N][H][D] bf16 seen as a 4D tensor (channel, head, token, item); box: 64 channels x 1 head x `tokens` x 1 item.
 // Tokens past N and heads past H read as zero.
 bool encode(CUtensorMap* m, const void* base, const Dims& d, int tokens) {
@@ -524,25 +544,30 @@ bool encode(CUtensorMap* m, const void* base, const Dims& d, int tokens) {
 }
 
 template <int D>
-cudaError_t local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s) {
-  LocalMaps m;
-  if (!encode(&m.x, a.x, d, TL) || !encode(&m.y, a.y, d, TL)) return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(lin_tc_local_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLocalSmem);
+cudaError_t local(const Dims& d, const LinLocalSets& a, uint32_t* status, cudaStream_t s) {
+  LocalMapSets m;
+  for (int i = 0; i < a.n; ++i)
+    if (!encode(&m.set[i].x, a.set[i].x, d, TL) || !encode(&m.set[i].y, a.set[i].y, d, TL)) return cudaErrorInvalidValue;
+  const auto kernel = a.n == 1 ? lin_tc_local_kernel<D, true> : lin_tc_local_kernel<D, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLocalSmem);
   if (e != cudaSuccess) return e;
-  const int groups = (d.H * D + 127) / 128;
-  lin_tc_local_kernel<D><<<dim3((unsigned)a.n_seg, groups, d.B), kLocalThreads, kLocalSmem, s>>>(m, a, status);
+  const dim3 grid((unsigned)(a.set[0].n_seg * a.n), (d.H * D + 127) / 128, d.B);
+  kernel<<<grid, kLocalThreads, kLocalSmem, s>>>(m, a, status);
   return cudaGetLastError();
 }
 
-template <int D, bool REV>
-cudaError_t map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s) {
-  MapMaps m;
-  if (!encode(&m.a, a.a, d, TM) || !encode(&m.b, a.b, d, TM) || !encode(&m.c, a.c, d, TM) || !encode(&m.out, a.out, d, TM))
-    return cudaErrorInvalidValue;
-  const cudaError_t e =
-      cudaFuncSetAttribute(lin_tc_map_kernel<D, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, MapSmem<D>::bytes);
+template <int D>
+cudaError_t map(const Dims& d, const LinMapSets& a, uint32_t* status, cudaStream_t s) {
+  MapMapSets m;
+  for (int i = 0; i < a.n; ++i)
+    if (!encode(&m.set[i].a, a.set[i].a, d, TM) || !encode(&m.set[i].b, a.set[i].b, d, TM) ||
+        !encode(&m.set[i].c, a.set[i].c, d, TM) || !encode(&m.set[i].out, a.set[i].out, d, TM))
+      return cudaErrorInvalidValue;
+  const auto kernel = a.n == 1 ? lin_tc_map_kernel<D, true> : lin_tc_map_kernel<D, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MapSmem<D>::bytes);
   if (e != cudaSuccess) return e;
-  lin_tc_map_kernel<D, REV><<<dim3((unsigned)((d.N + TM - 1) / TM), d.H, d.B), kMapThreads, MapSmem<D>::bytes, s>>>(m, a, status);
+  const dim3 grid((unsigned)((d.N + TM - 1) / TM * a.n), d.H, d.B);
+  kernel<<<grid, kMapThreads, MapSmem<D>::bytes, s>>>(m, a, status);
   return cudaGetLastError();
 }
 
@@ -558,18 +583,18 @@ int linear_tc_segment(const Dims& d) {
   return seg;
 }
 
-cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s) {
+cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalSets& a, uint32_t* status, cudaStream_t s) {
   return d.dk == 128 ? local<128>(d, a, status, s) : local<64>(d, a, status, s);
 }
-cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanArgs& a, bool local, cudaStream_t s) {
-  const dim3 grid(d.dk * d.dk / 8 / 128, d.B * d.H);
-  if (d.dk == 128) lin_tc_scan_kernel<128><<<grid, 128, 0, s>>>(a, local);
-  else lin_tc_scan_kernel<64><<<grid, 128, 0, s>>>(a, local);
+cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanSets& a, cudaStream_t s) {
+  const dim3 grid(d.dk * d.dk / 8 / 128 * a.n, d.B * d.H);
+  const auto kernel = d.dk == 128 ? (a.n == 1 ? lin_tc_scan_kernel<128, true> : lin_tc_scan_kernel<128, false>)
+                                  : (a.n == 1 ? lin_tc_scan_kernel<64, true> : lin_tc_scan_kernel<64, false>);
+  kernel<<<grid, 128, 0, s>>>(a);
   return cudaGetLastError();
 }
-cudaError_t launch_linear_tc_map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s) {
-  if (d.dk == 128) return a.reverse ? map<128, true>(d, a, status, s) : map<128, false>(d, a, status, s);
-  return a.reverse ? map<64, true>(d, a, status, s) : map<64, false>(d, a, status, s);
+cudaError_t launch_linear_tc_map(const Dims& d, const LinMapSets& a, uint32_t* status, cudaStream_t s) {
+  return d.dk == 128 ? map<128>(d, a, status, s) : map<64>(d, a, status, s);
 }
 
 }  // namespace kda

@@ -49,8 +49,8 @@ __device__ __forceinline__ uint32_t term_b(int p) { return (0x001102u >> (4 * p)
 // ---------------------------------------------------------------------------
 constexpr int kLocalSmem = 1024 + 6 * 16384;
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2) lin_tc32_local_kernel(LinLocalArgs a, uint32_t* status) {
+template <int D, bool ONE>
+__global__ void __launch_bounds__(kThreads, 2) lin_tc32_local_kernel(const __grid_constant__ LinLocalSets sets, uint32_t* status) {
   extern __shared__ uint8_t dyn[];
   __shared__ uint64_t ready, done;
   __shared__ uint32_t tmem_slot;
@@ -60,7 +60,9 @@ __global__ void __launch_bounds__(kThreads, 2) lin_tc32_local_kernel(LinLocalArg
   volatile int* abort_flag = &abort_slot;
   const int tid = threadIdx.x, warp = tid / 32;
   constexpr int HP = 128 / D;   // heads per CTA
-  const int seg = blockIdx.x, h0 = blockIdx.y * HP, b = blockIdx.z;
+  const int per_set = ONE ? gridDim.x : gridDim.x / sets.n, which = ONE ? 0 : blockIdx.x / per_set;
+  const LinLocalArgs& a = sets.set[which];
+  const int seg = blockIdx.x - which * per_set, h0 = blockIdx.y * HP, b = blockIdx.z;
   const int64_t s0 = (int64_t)seg * kSeg, len = item_tokens(a.lengths, b, a.N);
   const int n_tok = (int)max((int64_t)0, min(len - s0, (int64_t)kSeg)), n_tiles = (n_tok + TK - 1) / TK;
   if (tid == 0) {
@@ -186,8 +188,7 @@ template <int D> struct MapSmem {
 template <int D> constexpr uint32_t kMapTmem = D == 128 ? 512 : 256;
 
 template <int D, bool REV>
-__global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2) lin_tc32_map_kernel(const __grid_constant__ CUtensorMap out_map,
-                                                                                 LinMapArgs a, uint32_t* status) {
+__device__ __forceinline__ void map_tile(const CUtensorMap& out_map, const LinMapArgs& a, int tile, uint32_t* status) {
   using L = MapSmem<D>;
   extern __shared__ uint8_t dyn[];
   __shared__ uint64_t bar_b, bar_s, bar_p, bar_o;
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2) lin_tc32_map_kerne
   volatile int* abort_flag = &abort_slot;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int h = blockIdx.y, b = blockIdx.z;
-  const int64_t i0 = (int64_t)blockIdx.x * TM, len = item_tokens(a.lengths, b, a.N);
+  const int64_t i0 = (int64_t)tile * TM, len = item_tokens(a.lengths, b, a.N);
   const int seg = (int)(i0 / kSeg);
   const int64_t s0 = (int64_t)seg * kSeg, end = min(len, s0 + kSeg), stride = (int64_t)a.H * D;
   const int64_t head = (int64_t)b * a.N * stride + (int64_t)h * D;
@@ -424,30 +425,51 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2) lin_tc32_map_kerne
   if (warp == 8) tmem_dealloc(tm_s, kMapTmem<D>);
 }
 
+struct OutMaps { CUtensorMap set[3]; };
+
+// ONE: the forward pass's map alone; otherwise the backward pass's three.
+template <int D, bool ONE>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2) lin_tc32_map_kernel(const __grid_constant__ OutMaps outs,
+                                                                                 const __grid_constant__ LinMapSets sets,
+                                                                                 uint32_t* status) {
+  if constexpr (ONE) {
+    map_tile<D, false>(outs.set[0], sets.set[0], blockIdx.x, status);
+  } else {
+    const int per_set = gridDim.x / sets.n, which = blockIdx.x / per_set, tile = blockIdx.x % per_set;
+    if (sets.set[which].reverse) map_tile<D, true>(outs.set[which], sets.set[which], tile, status);
+    else map_tile<D, false>(outs.set[which], sets.set[which], tile, status);
+  }
+}
+
 template <int D>
-cudaError_t local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(lin_tc32_local_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLocalSmem);
+cudaError_t local(const Dims& d, const LinLocalSets& a, uint32_t* status, cudaStream_t s) {
+  const auto kernel = a.n == 1 ? lin_tc32_local_kernel<D, true> : lin_tc32_local_kernel<D, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLocalSmem);
   if (e != cudaSuccess) return e;
-  lin_tc32_local_kernel<D><<<dim3((unsigned)a.n_seg, (d.H * D + 127) / 128, d.B), kThreads, kLocalSmem, s>>>(a, status);
+  const dim3 grid((unsigned)(a.set[0].n_seg * a.n), (d.H * D + 127) / 128, d.B);
+  kernel<<<grid, kThreads, kLocalSmem, s>>>(a, status);
   return cudaGetLastError();
 }
 
-template <int D, bool REV>
-cudaError_t map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s) {
+template <int D>
+cudaError_t map(const Dims& d, const LinMapSets& a, uint32_t* status, cudaStream_t s) {
   // out [B][N][H][D] seen as a 4D tensor; box: 32 channels x 1 head x 128 tokens x 1 item
   const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return cudaErrorInvalidValue;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)d.H, (cuuint64_t)d.N, (cuuint64_t)d.B};
   const cuuint64_t strides[3] = {(cuuint64_t)D * 4, (cuuint64_t)d.H * D * 4, (cuuint64_t)d.N * d.H * D * 4};
   const cuuint32_t box[4] = {32u, 1u, (cuuint32_t)TM, 1u}, estr[4] = {1u, 1u, 1u, 1u};
-  CUtensorMap m;
-  if (enc(&m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
-  const cudaError_t e =
-      cudaFuncSetAttribute(lin_tc32_map_kernel<D, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, MapSmem<D>::bytes);
+  OutMaps m;
+  for (int i = 0; i < a.n; ++i)
+    if (enc(&m.set[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.set[i].out, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  const auto kernel = a.n == 1 ? lin_tc32_map_kernel<D, true> : lin_tc32_map_kernel<D, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MapSmem<D>::bytes);
   if (e != cudaSuccess) return e;
-  lin_tc32_map_kernel<D, REV><<<dim3((unsigned)((d.N + TM - 1) / TM), d.H, d.B), kThreads, MapSmem<D>::bytes, s>>>(m, a, status);
+  const dim3 grid((unsigned)((d.N + TM - 1) / TM * a.n), d.H, d.B);
+  kernel<<<grid, kThreads, MapSmem<D>::bytes, s>>>(m, a, status);
   return cudaGetLastError();
 }
 
@@ -455,12 +477,11 @@ cudaError_t map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream
 
 int linear_tc32_segment() { return kSeg; }
 
-cudaError_t launch_linear_tc32_local(const Dims& d, const LinLocalArgs& a, uint32_t* status, cudaStream_t s) {
+cudaError_t launch_linear_tc32_local(const Dims& d, const LinLocalSets& a, uint32_t* status, cudaStream_t s) {
   return d.dk == 128 ? local<128>(d, a, status, s) : local<64>(d, a, status, s);
 }
-cudaError_t launch_linear_tc32_map(const Dims& d, const LinMapArgs& a, uint32_t* status, cudaStream_t s) {
-  if (d.dk == 128) return a.reverse ? map<128, true>(d, a, status, s) : map<128, false>(d, a, status, s);
-  return a.reverse ? map<64, true>(d, a, status, s) : map<64, false>(d, a, status, s);
+cudaError_t launch_linear_tc32_map(const Dims& d, const LinMapSets& a, uint32_t* status, cudaStream_t s) {
+  return d.dk == 128 ? map<128>(d, a, status, s) : map<64>(d, a, status, s);
 }
 
 }  // namespace kda
