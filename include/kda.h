@@ -248,7 +248,9 @@ int kda_chunk_fwd_noalloc(const kda_problem* p, kda_dtype dtype,
  * valid and have no effect, KDA_FLAG_REUSE_RECORDS and KDA_FLAG_QKV_F16 are rejected, and B * H may be at most
  * 65535.  The aliasing rule is checked: an output that shares bytes with an input or another output returns
  * KDA_ERR_INVALID_ARG, except where a call says that it works in place.  Results do not depend on timing: no
- * sum's order varies between runs. */
+ * sum's order varies between runs.  A workspace serves one call at a time: calls that share one run on one stream.
+ * The bounded waits of the linear-attention kernels record KDA_ERR_TIMEOUT in the workspace's status word
+ * (kda_read_status); the outputs are then not valid. */
 
 /* Interleaved pairs: pair j of a head is (2j, 2j+1) instead of (j, j + d/2). */
 #define KDA_ROPE_INTERLEAVED 1u
@@ -296,8 +298,12 @@ int kda_layernorm_bwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* d
  * nothing, -inf keeps the token alone); initial_state, final_state: [B, H, d, d] fp32 or NULL.
  * lengths: [B] int32 or NULL (N each).  Item b's sequence is its first lengths[b] tokens (clamped to 0..N): what
  * q, k, v hold behind them is not used, whatever it is, o is zero there, and final_state is the state after the
- * item's own last token.  Inputs within the sequences must be finite.  The workspace is
- * kda_linear_workspace_bytes(p, dtype) bytes, 256-byte aligned.  Returns a kda_status. */
+ * item's own last token.  Inputs within the sequences must be finite.
+ * The recurrence is evaluated in segments of 128 to 512 tokens on the tensor cores.  For bf16 problems every decayed
+ * score, and the state that enters a segment, is rounded once to bf16 for its product; the states themselves and
+ * final_state keep fp32 accuracy.  fp32 problems keep it throughout.  The workspace is
+ * kda_linear_workspace_bytes(p, dtype) bytes, 256-byte aligned (4 d^2 bytes per batch item, head and segment beside
+ * the status word).  Returns a kda_status. */
 size_t kda_linear_workspace_bytes(const kda_problem* p, kda_dtype dtype);
 int kda_linear_fwd(const kda_problem* p, kda_dtype dtype,
                    const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,

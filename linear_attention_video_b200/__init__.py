@@ -1,5 +1,7 @@
 """Python binding of libkda.so: the B200 (sm_100a) forward pass of the
-modality-aware short convolution followed by the Kimi Delta Attention scan.
+modality-aware short convolution followed by the Kimi Delta Attention scan,
+their backward pass, and the operators beside them (linear attention with a
+decay per head, rotary positions, layer norm).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI declared in ``include/kda.h``.  Tensors are torch
