@@ -245,8 +245,8 @@ int kda_chunk_fwd_noalloc(const kda_problem* p, kda_dtype dtype,
  * attention with that decay (whole sequences, gradients, single tokens), and the layer norm in front of the
  * mixer.  The pages have no counterpart.  They follow the conventions above; of a kda_problem they use the shape
  * (B, H, dk = dv of 64 or 128, and the token count of text_len and the grid); its conv and scan options must be
- * valid and have no effect, KDA_FLAG_REUSE_RECORDS and KDA_FLAG_QKV_F16 are rejected, and B * H may be at most
- * 65535.  The aliasing rule is checked: an output that shares bytes with an input or another output returns
+ * valid and have no effect, KDA_FLAG_REUSE_RECORDS and KDA_FLAG_QKV_F16 are rejected, and B and H may be at most
+ * 65535 each.  The aliasing rule is checked: an output that shares bytes with an input or another output returns
  * KDA_ERR_INVALID_ARG, except where a call says that it works in place.  Results do not depend on timing: no
  * sum's order varies between runs.  A workspace serves one call at a time: calls that share one run on one stream.
  * The bounded waits of the linear-attention kernels record KDA_ERR_TIMEOUT in the workspace's status word

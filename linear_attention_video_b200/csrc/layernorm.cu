@@ -80,13 +80,104 @@ template <int V> __device__ __forceinline__ void load_par(const float* p, int c,
   }
 }
 
+// Two fp32 operations in one instruction: half the issue slots, which is what holds the bf16 rows.
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+// (x, y) = (a, b) * (c, d) + (x, y)
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float c, float d) {
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 r, {%4, %5};\n\t"
+      "fma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y) : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+// The same over V elements, single ones where V is odd.  x += y; x *= y; z += x y.
+template <int V> __device__ __forceinline__ void add_v(float (&x)[V], const float (&y)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) add2(x[j], x[j + 1], y[j], y[j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] += y[j];
+  }
+}
+template <int V> __device__ __forceinline__ void add_s(float (&x)[V], float y) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) add2(x[j], x[j + 1], y, y);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] += y;
+  }
+}
+template <int V> __device__ __forceinline__ void mul_v(float (&x)[V], const float (&y)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) mul2(x[j], x[j + 1], y[j], y[j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] *= y[j];
+  }
+}
+template <int V> __device__ __forceinline__ void mul_s(float (&x)[V], float y) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) mul2(x[j], x[j + 1], y, y);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] *= y;
+  }
+}
+template <int V> __device__ __forceinline__ void fma_v(float (&z)[V], const float (&x)[V], const float (&y)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) fma2(z[j], z[j + 1], x[j], x[j + 1], y[j], y[j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) z[j] = fmaf(x[j], y[j], z[j]);
+  }
+}
+template <int V> __device__ __forceinline__ void fma_s(float (&z)[V], const float (&x)[V], float y) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) fma2(z[j], z[j + 1], x[j], x[j + 1], y, y);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) z[j] = fmaf(x[j], y, z[j]);
+  }
+}
+// Two strands of a lane's sum: sum over V elements into (lo, hi), x or x y each.
+template <int V> __device__ __forceinline__ void sum_v(float (&s)[2], const float (&x)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) add2(s[0], s[1], x[j], x[j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[0] += x[j];
+  }
+}
+template <int V> __device__ __forceinline__ void dot_v(float (&s)[2], const float (&x)[V], const float (&y)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) fma2(s[0], s[1], x[j], x[j + 1], y[j], y[j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[0] = fmaf(x[j], y[j], s[0]);
+  }
+}
+
 // A row belongs to G lanes (a power of two, 8..1024) with E elements each, in vectors of V, and a group of lanes
 // takes R rows at a time: R rows' loads are in flight together and share one reading of the weight.
 template <int G> struct Shape {
   static constexpr int threads = G < 128 ? 128 : G;
   static constexpr int groups = threads / G;
 };
-constexpr int kFwdThreads = 1024, kBwdThreads = 512;   // resident threads per SM that registers must allow
+// Resident threads per SM that registers must allow.  Backward: 640 would spill (33,272 x 2048 bf16: 123 us against 83).
+constexpr int kFwdThreads = 1024, kBwdThreads = 512;
 constexpr int ctas_of(int threads, int resident) { return threads < resident ? resident / threads : 1; }
 
 // Sums of K values over the G lanes of a group; every thread of the CTA calls it.
@@ -157,31 +248,29 @@ __global__ void __launch_bounds__(Shape<G>::threads, ctas_of(Shape<G>::threads, 
   float s[R], mean[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    s[r] = 0.f;
+    float t[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float v[V];
       widen(cur[r][i], v);
-#pragma unroll
-      for (int j = 0; j < V; ++j) s[r] += v[j];
+      sum_v<V>(t, v);
     }
+    s[r] = t[0] + t[1];
   }
   group_sum<G>(s, scratch, group, lane);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     mean[r] = s[r] * inv;
-    s[r] = 0.f;
+    float t[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if ((i * G + lane) * V < a.cols) {
         float v[V];
         widen(cur[r][i], v);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float d = v[j] - mean[r];
-          s[r] = fmaf(d, d, s[r]);
-        }
+        add_s<V>(v, -mean[r]);
+        dot_v<V>(t, v, v);
       }
+    s[r] = t[0] + t[1];
   }
   group_sum<G>(s, scratch, group, lane);
 #pragma unroll
@@ -207,8 +296,11 @@ __global__ void __launch_bounds__(Shape<G>::threads, ctas_of(Shape<G>::threads, 
       if (row0 + r >= a.rows) break;
       float v[V], o[V];
       widen(cur[r][i], v);
+      add_s<V>(v, -mean[r]);
+      mul_s<V>(v, s[r]);
 #pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = fmaf((v[j] - mean[r]) * s[r], w[j], b[j]);
+      for (int j = 0; j < V; ++j) o[j] = b[j];
+      fma_v<V>(o, v, w);
       store_vec<V>(y + (int64_t)r * a.cols + c, o);
     }
   }
@@ -253,23 +345,21 @@ __global__ void __launch_bounds__(Shape<G>::threads, ctas_of(Shape<G>::threads, 
     for (int r = 0; r < R; ++r) {
       const float mean = nm[r];
       rstd[r] = nr[r];
-      s[2 * r] = s[2 * r + 1] = 0.f;
+      float t[2] = {0.f, 0.f}, u[2] = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
+      for (int i = 0; i < NV; ++i) {   // columns past the row have dy = 0
         widen(nx[r][i], h[r][i]);
         widen(ny[r][i], g[r][i]);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {   // columns past the row have dy = 0
-          float& hh = h[r][i][j];
-          float& gg = g[r][i][j];
-          hh = (hh - mean) * rstd[r];
-          dw[i][j] = fmaf(gg, hh, dw[i][j]);
-          db[i][j] += gg;
-          gg *= w[i][j];
-          s[2 * r] += gg;
-          s[2 * r + 1] = fmaf(gg, hh, s[2 * r + 1]);
-        }
+        add_s<V>(h[r][i], -mean);
+        mul_s<V>(h[r][i], rstd[r]);
+        fma_v<V>(dw[i], g[r][i], h[r][i]);
+        add_v<V>(db[i], g[r][i]);
+        mul_v<V>(g[r][i], w[i]);
+        sum_v<V>(t, g[r][i]);
+        dot_v<V>(u, g[r][i], h[r][i]);
       }
+      s[2 * r] = t[0] + t[1];
+      s[2 * r + 1] = u[0] + u[1];
     }
     get(row0 + stride);
     group_sum<G>(s, scratch, group, lane);
@@ -284,7 +374,9 @@ __global__ void __launch_bounds__(Shape<G>::threads, ctas_of(Shape<G>::threads, 
         if (c >= a.cols) continue;
         float o[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) o[j] = fmaf(g[r][i][j], rstd[r], fmaf(h[r][i][j], mgh, mg));
+        for (int j = 0; j < V; ++j) o[j] = mg;
+        fma_s<V>(o, h[r][i], mgh);
+        fma_s<V>(o, g[r][i], rstd[r]);
         store_vec<V>(dx + (int64_t)r * a.cols + c, o);
       }
     }
@@ -373,7 +465,7 @@ cudaError_t fwd(const NormFwdArgs& a, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-// Backward: 16 elements of a row per lane and one row at a time (33,272 x 2048 bf16: 82 us; 8 and two rows 83 us, the
+// Backward: 16 elements of a row per lane and one row at a time (33,272 x 2048 bf16: 80 us; 8 and two rows 83 us, the
 // reductions then cost a third of the instructions; 16 and two rows 151 us, out of registers).  Scalar accesses take
 // 8 and two rows (2047 columns: 116 us against 160).
 int lanes_for(int cols, int e) {

@@ -41,7 +41,8 @@ template <bool ONE>
 __global__ void __launch_bounds__(128) lin_scan_kernel(const __grid_constant__ LinScanSets sets) {
   const int per_set = ONE ? gridDim.x : gridDim.x / sets.n, which = ONE ? 0 : blockIdx.x / per_set;
   const LinScanArgs& a = sets.set[which];
-  const int bh = blockIdx.y, h = bh % a.H, b = bh / a.H;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int64_t bh = (int64_t)b * a.H + h;
   const int64_t e = ((int64_t)(blockIdx.x - which * per_set) * 128 + threadIdx.x) * 4;   // element of the D x D state
   const int64_t dd = a.dd, len = item_tokens(a.lengths, b, a.N);
   const float ld = a.log_decay[h];
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(128) lin_scan_kernel(const __grid_constant__ L
   const Factor whole = segment_factor(ld, a.seg), part = segment_factor(ld, len % a.seg);
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.initial) S = *reinterpret_cast<const float4*>(a.initial + bh * dd + e);
-  float* p = a.states + (int64_t)bh * a.n_seg * dd + e;
+  float* p = a.states + bh * a.n_seg * dd + e;
   constexpr int U = ONE ? 8 : 4;   // states fetched at once (33,272 x 16 x 128: 86 us, 4 102; two sets 178, 8 285)
   for (int c0 = 0; c0 < a.n_seg; c0 += U) {
     float4 loc[U];
@@ -137,7 +138,7 @@ template <typename F> cudaError_t dispatch(const Dims& d, kda_dtype dt, F f) {
 
 cudaError_t launch_scan(const Dims& d, const LinScanSets& a, cudaStream_t s) {
   const auto kernel = a.n == 1 ? lin_scan_kernel<true> : lin_scan_kernel<false>;
-  kernel<<<dim3((unsigned)(a.set[0].dd / 512 * a.n), d.B * d.H), 128, 0, s>>>(a);
+  kernel<<<dim3((unsigned)(a.set[0].dd / 512 * a.n), d.H, d.B), 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -219,18 +219,19 @@ __global__ void __launch_bounds__(128) lin_tc_scan_kernel(const __grid_constant_
   constexpr int kPerSet = D * D / 8 / 128;
   const LinScanArgs& a = sets.set[ONE ? 0 : blockIdx.x / kPerSet];
   const bool local = a.local;
-  const int bh = blockIdx.y, h = bh % a.H, b = bh / a.H;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int64_t bh = (int64_t)b * a.H + h;
   const int e = blockIdx.x % kPerSet * 128 + threadIdx.x, r = e / (D / 8), c8 = e % (D / 8);
   const int64_t len = item_tokens(a.lengths, b, a.N), last = len / a.seg;
   const float ld = a.log_decay[h];
   const Factor whole = segment_factor(ld, a.seg), part = segment_factor(ld, len % a.seg);
   float S[8] = {};
   if (a.initial) {
-    const float4* p = reinterpret_cast<const float4*>(a.initial + (int64_t)bh * D * D + r * D + c8 * 8);
+    const float4* p = reinterpret_cast<const float4*>(a.initial + bh * D * D + r * D + c8 * 8);
     const float4 u = p[0], v = p[1];
     S[0] = u.x; S[1] = u.y; S[2] = u.z; S[3] = u.w; S[4] = v.x; S[5] = v.y; S[6] = v.z; S[7] = v.w;
   }
-  uint8_t* p = reinterpret_cast<uint8_t*>(a.states + (int64_t)bh * a.n_seg * D * D) + image_off(D, r, c8);
+  uint8_t* p = reinterpret_cast<uint8_t*>(a.states + bh * a.n_seg * D * D) + image_off(D, r, c8);
   constexpr int LO = D * D * 2;
   for (int c0 = 0; c0 < a.n_seg; c0 += U) {
     float4 x[U], y[U];
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(128) lin_tc_scan_kernel(const __grid_constant_
     }
   }
   if (a.final) {
-    float4* q = reinterpret_cast<float4*>(a.final + (int64_t)bh * D * D + r * D + c8 * 8);
+    float4* q = reinterpret_cast<float4*>(a.final + bh * D * D + r * D + c8 * 8);
     q[0] = make_float4(S[0], S[1], S[2], S[3]);
     q[1] = make_float4(S[4], S[5], S[6], S[7]);
   }
@@ -591,7 +592,7 @@ cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalSets& a, uint32_
 template <int D, int U>
 static void scan(const Dims& d, const LinScanSets& a, cudaStream_t s) {
   const auto kernel = a.n == 1 ? lin_tc_scan_kernel<D, true, U> : lin_tc_scan_kernel<D, false, U>;
-  kernel<<<dim3(D * D / 8 / 128 * a.n, d.B * d.H), 128, 0, s>>>(a);
+  kernel<<<dim3(D * D / 8 / 128 * a.n, d.H, d.B), 128, 0, s>>>(a);
 }
 cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanSets& a, cudaStream_t s) {
   const bool few = a.set[0].n_seg <= 4;

@@ -65,7 +65,7 @@ int make_shape(const kda_problem* p, kda_dtype dt, kda::Dims* d) {
   const int st = kda::validate_problem(p, dt, d);
   if (st) return st;
   if (d->reuse_records || d->qkv_f16) return KDA_ERR_INVALID_ARG;
-  if (d->B > 65535 || d->H > 65535 || (int64_t)d->B * d->H > 65535) return KDA_ERR_UNSUPPORTED;   // grid axes
+  if (d->B > 65535 || d->H > 65535) return KDA_ERR_UNSUPPORTED;   // grid axes
   return KDA_OK;
 }
 

@@ -57,7 +57,7 @@ def test_linear_refusals(call):
     p = _p()
     assert call(_p(d=96)) == UNSUPPORTED and call(_p(d=64, dv=128)) == UNSUPPORTED
     assert call(_p(B=0)) == INVALID and call(_p(text_len=-1)) == INVALID and call(_p(grid=(1, 0, 4))) == INVALID
-    assert call(_p(B=256, H=256)) == UNSUPPORTED
+    assert call(_p(B=65536)) == UNSUPPORTED and call(_p(H=65536)) == UNSUPPORTED
     assert call(p, dt=2) == INVALID
     assert call(_p(reuse_records=True)) == INVALID
     assert call(_p(d=128, qkv_f16=True), dt=0) == INVALID
