@@ -280,7 +280,8 @@ int kda_rope_bwd(const kda_problem* p, const kda_rope* rope, kda_dtype dtype,
 /* Layer norm over the last axis of x [rows, cols]: y = (x - mean) * rstd * weight + bias with
  * rstd = (mean of (x - mean)^2 + eps)^(-1/2), statistics in fp32.  x and y have dtype; weight and bias are
  * [cols] fp32 or NULL (1 and 0); mean and rstd, [rows] fp32 or NULL, receive the statistics that the backward
- * pass takes.  cols up to 16384 (beyond: KDA_ERR_UNSUPPORTED); rows may be 0.  Returns a kda_status. */
+ * pass takes.  cols up to 16384 (beyond: KDA_ERR_UNSUPPORTED); rows may be 0 (x, y and
+ * the like may then be NULL).  Returns a kda_status. */
 int kda_layernorm_fwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* x, const float* weight,
                       const float* bias, float eps, void* y, float* mean, float* rstd, void* stream);
 

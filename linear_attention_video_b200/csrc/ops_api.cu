@@ -15,9 +15,10 @@ struct Span {   // an argument's address range
   size_t bytes;
 };
 
+// A required argument has an address, unless the problem has none of its elements (an empty tensor has no address).
 int check_aligned(std::initializer_list<Span> required, std::initializer_list<Span> optional) {
   for (const Span& s : required)
-    if (!s.p) return KDA_ERR_INVALID_ARG;
+    if (!s.p && s.bytes) return KDA_ERR_INVALID_ARG;
   for (const auto* list : {&required, &optional})
     for (const Span& s : *list)
       if (reinterpret_cast<uintptr_t>(s.p) & 15u) return KDA_ERR_MISALIGNED;

@@ -431,6 +431,16 @@ def test_layernorm_constant_rows_and_no_rows(kda):
     assert not dw.any() and not db.any()
 
 
+def test_layernorm_of_tensors_without_rows(kda):
+    e, s = torch.empty(2, 0, 16, device="cuda"), torch.empty(2, 0, device="cuda")
+    y, w = torch.empty_like(e), torch.ones(16, device="cuda")
+    kda.kda_layernorm_fwd(e, y, w, w, 1e-5, s, torch.empty_like(s))
+    dw, db = torch.full((16,), 7.0, device="cuda"), torch.full((16,), 7.0, device="cuda")
+    kda.kda_layernorm_bwd(e, e.clone(), s, s.clone(), y, kda.alloc_layernorm_bwd_workspace(0, 16), w, dw, db)
+    torch.cuda.synchronize()
+    assert not dw.any() and not db.any()
+
+
 def test_layernorm_many_rows(kda):
     g = gen(77)
     x, dy = randn(g, 100003, 48, dtype=torch.bfloat16), randn(g, 100003, 48, dtype=torch.bfloat16)

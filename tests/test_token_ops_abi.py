@@ -131,6 +131,14 @@ def test_layernorm_refusals():
         kda.alloc_layernorm_bwd_workspace(4, 20000)
 
 
+def test_layernorm_of_no_rows_takes_empty_tensors():
+    """A tensor without elements has no address; only what the call would not read or write may lack one."""
+    assert _norm(rows=0, x=None, y=None, m=None, r=None) == kda.KDA_OK and kda.kda_last_launch_count() == 0
+    none = dict(rows=0, dy=None, x=None, m=None, r=None, dx=None)
+    assert _norm_bwd(**none, dw=None, db=None) == kda.KDA_OK and kda.kda_last_launch_count() == 0
+    assert _norm(rows=0, x=4, y=None) == MISALIGNED and _norm_bwd(**none, ws=None) == WORKSPACE
+
+
 def test_a_refused_call_launches_nothing():
     assert _linear(_p(), q=None) and kda.kda_last_launch_count() == 0
     assert _norm(cols=0) and kda.kda_last_launch_count() == 0
