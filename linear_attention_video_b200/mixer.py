@@ -188,9 +188,12 @@ class LinearLayer:
 
     def backward(self, x, dy, lengths=None, positions=None):
         """Gradients of sum(dy * self(x)): that of x, and a dict of the weights'.  The forward pass up to the
-        attention is computed again; nothing of it has to be kept."""
+        attention is computed again; nothing of it has to be kept.  Tokens behind an item's length change nothing."""
         B, N, D = x.shape
         rows = B * N
+        if lengths is not None:   # the weights' products run over all rows: 0 times what stands there has to be 0
+            behind = (torch.arange(N, device=x.device) >= lengths.view(B, 1)).unsqueeze(-1)
+            x, dy = x.masked_fill(behind, 0), dy.masked_fill(behind, 0)
         mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
         h, q, k, v = self._qkv(self.p, x, positions, (mean, rstd))
         o = torch.empty_like(v)

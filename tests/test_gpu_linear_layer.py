@@ -78,6 +78,21 @@ def test_forward_and_gradients(layer):
             assert rel(g, w[name].grad) <= BWD, (name, rel(g, w[name].grad))
 
 
+@pytest.mark.parametrize("second", [0, 211])
+def test_what_stands_behind_a_sequence_reaches_no_output(layer, second):
+    """NaN and infinities there change no bit of the output and of any gradient."""
+    x, dy = _x(3), _x(4)
+    lengths = torch.tensor([N, second], dtype=torch.int32, device="cuda")
+    junk_x, junk_dy = x.clone(), dy.clone()
+    junk_x[1, second:], junk_dy[1, second:] = math.nan, math.inf
+    assert torch.equal(layer(junk_x, lengths=lengths), layer(x, lengths=lengths))
+    dx, grads = layer.backward(x, dy, lengths=lengths)
+    got, got_grads = layer.backward(junk_x, junk_dy, lengths=lengths)
+    assert torch.equal(got, dx) and not got[1, second:].any()
+    for name, g in grads.items():
+        assert torch.isfinite(g).all() and torch.equal(got_grads[name], g), name
+
+
 def test_prompts_then_tokens(layer):
     """Prompts of different lengths, then five tokens each from the states they left, against whole sequences."""
     from linear_attention_video_b200 import mixer
