@@ -234,8 +234,8 @@ __device__ __forceinline__ void fetch(const void* base, int64_t row0, int64_t ro
 // Forward: a row stays as fetched and is widened in each of the three passes over it: one instruction per element and
 // pass, against twice the registers.  A lane takes four columns at a time, whose weights and biases are one 16-byte
 // access each (of eight they would be two, half a line apart: the L1 cache, which serves them for every row, is then
-// 75% busy).  One row per group and many CTAs: 33,272 x 2048 bf16 in 51 us, against 57 with two rows at a time and 54
-// with a persistent grid that fetches ahead; fp32 runs at the bandwidth of a copy either way (84 us).
+// 75% busy).  One row per group and many CTAs: 33,272 x 2048 bf16 in 51 us, the same with two rows at a time, 55 to 57
+// with a warp per row and 54 with a persistent grid that fetches ahead; fp32 runs at a copy's bandwidth (84 us).
 template <typename T, int V, int NV, int G, int R>
 __global__ void __launch_bounds__(Shape<G>::threads, ctas_of(Shape<G>::threads, kFwdThreads)) norm_fwd_kernel(NormFwdArgs a) {
   using S = Shape<G>;
