@@ -455,16 +455,10 @@ __device__ __forceinline__ void map_tile(const MapMaps& maps, const LinMapArgs& 
         }
         tmem_st16(tm_s + lanes + 16 * g, p);
       }
-      if (n_valid < TM) {   // c behind the end may hold anything, and 0 x NaN is NaN
-        ok = warp_wait(&full_c, (has_state + t) & 1, abort_flag);
-        for (int i = tid + n_valid * (D / 8); i < TM * (D / 8); i += 128)
-          *reinterpret_cast<uint4*>(cs + image_off(TM, i / (D / 8), i % (D / 8))) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async();
-      }
       if (t == 0 && has_state) {   // O = a X, row by row lam^e(i) of it, before the tiles are added
         const float w = decay_pow(ld, REV ? max((int64_t)0, end - 1 - (i0 + row)) : i0 + row - s0 + 1);
-        ok = ok && warp_wait(&bar_o, 0, abort_flag);
-        if (!ok) break;
+        ok = warp_wait(&bar_o, 0, abort_flag);
+        if (!ok) { tmem_wait_st(); break; }
         fence_after_sync();
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -476,6 +470,17 @@ __device__ __forceinline__ void map_tile(const MapMaps& maps, const LinMapArgs& 
           for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * w);
           tmem_st32(tm_o + lanes + c, u);
         }
+      }
+      // A wait for a phase holds only once the phase before is over.  Of full_c, load 0 is X where there is a state and
+      // c of tile t is load has_state + t.  Load has_state + t - 1 is over here: at t = 0 it is X, which the product
+      // behind bar_o has read (waited for above); at t > 0 the scores of this tile, whose bar_s every row has waited
+      // for, were issued after O += P c of the tile before.
+      if (n_valid < TM) {   // c behind the end may hold anything, and 0 x NaN is NaN
+        ok = warp_wait(&full_c, (has_state + t) & 1, abort_flag);
+        if (!ok) { tmem_wait_st(); break; }
+        for (int i = tid + n_valid * (D / 8); i < TM * (D / 8); i += 128)
+          *reinterpret_cast<uint4*>(cs + image_off(TM, i / (D / 8), i % (D / 8))) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async();
       }
       tmem_wait_st();
       fence_before_sync();
