@@ -300,9 +300,10 @@ int kda_layernorm_bwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* d
  * lengths: [B] int32 or NULL (N each).  Item b's sequence is its first lengths[b] tokens (clamped to 0..N): what
  * q, k, v hold behind them is not used, whatever it is, o is zero there, and final_state is the state after the
  * item's own last token.  Inputs within the sequences must be finite.
- * The recurrence is evaluated in segments of 128 to 512 tokens on the tensor cores.  For bf16 problems every decayed
- * score, and the state that enters a segment, is rounded once to bf16 for its product; the states themselves and
- * final_state keep fp32 accuracy.  fp32 problems keep it throughout.  The workspace is
+ * The recurrence is evaluated in segments of 128 to 512 tokens on the tensor cores.  Of a bf16 problem the outputs alone
+ * are rounded to bf16: decayed scores, and the states that enter segments, go into their products as two bf16 terms
+ * (2^-16 of each is left out); the states themselves and final_state keep fp32 accuracy.  fp32 problems keep it
+ * throughout.  The workspace is
  * kda_linear_workspace_bytes(p, dtype) bytes, 256-byte aligned (4 d^2 bytes per batch item, head and segment beside
  * the status word).  Returns a kda_status. */
 size_t kda_linear_workspace_bytes(const kda_problem* p, kda_dtype dtype);

@@ -8,15 +8,18 @@
 // column's place cc in its group of 32, lam^(i-j) = lam^(i - group's last) * lam^(31-cc), a factor per (row, group)
 // times one of 32 registers, both at most 1.  Only the 32 x 32 blocks on the diagonal look lam^(i-j) up.
 //
-// What is rounded: the decayed scores and the state that enters a segment go to bf16 for their products with c and a,
-// as in any attention on these units: each term of an output is rounded once, by at most 2^-8 of it (half a step),
-// like the output itself; together 1.4 times the output's own rounding at random.  The states stay fp32 from segment
-// to segment, and the sums that become a state are taken of three bf16 terms (24 bits), because states are fp32
-// results.  All sums are fp32.
+// What is rounded: an output, once, to bf16.  A decayed score and a state that enters a segment go into their products
+// with c and a as two bf16 terms, which leaves 2^-16 of each (a state is an fp32 argument and the past of every later
+// token, and the single-token call reads it in fp32).  The error against fp64 is that of rounding the exact outputs,
+// 1.66e-3 of their norm at random.  One term each would give 2.35e-3; 33,272 x 16 x 128 forward takes 292 us as it is,
+// 270 with scores of one term, 278 with states of one, 258 with both.  The states stay fp32 from segment to segment, and
+// the sums that become a state are taken of three bf16 terms (24 bits), because states are fp32 results.
+// All sums are fp32.
 //
-// State images.  Between scan and map a state is a bf16 matrix in the 128-byte-swizzled panels that the tensor core
-// reads, so a CTA fetches it with one bulk copy.  Of a segment's fp32 local state, four of eight columns lie where
-// the image's eight will be and four as far behind it, so the scan works in place.
+// State images.  Between scan and map a state is two bf16 matrices, its first and second terms, in the
+// 128-byte-swizzled panels that the tensor core reads, so a CTA fetches each with one bulk copy.  Of a segment's fp32
+// local state, four of eight columns lie where the first image's eight will be and four where the second's will be, so
+// the scan works in place.
 #include "linear_tc.cuh"
 
 namespace kda {
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __
 // ---------------------------------------------------------------------------
 // scan
 // ---------------------------------------------------------------------------
-// A thread takes 8 columns of one row: 32 bytes of the local state, 16 of the image over them.
+// A thread takes 8 columns of one row: 32 bytes of the local state, 16 each of the two images over them.
 // U local states are fetched at once: 8 (189,272 tokens x 16 x 128: 99 us, with 4 123), or 4 where there are no more
 // and fewer registers let more CTAs run at once (8 x 2000 x 16 x 128: 10 us, with 8 13).
 template <int D, bool ONE, int U>
@@ -249,7 +252,16 @@ __global__ void __launch_bounds__(128) lin_tc_scan_kernel(const __grid_constant_
       if (c0 + u >= a.n_seg) break;
       const int c = a.reverse ? a.n_seg - 1 - c0 - u : c0 + u;
       uint8_t* s = p + (int64_t)c * D * D * 4;
-      *reinterpret_cast<uint4*>(s) = make_uint4(pack2(S[0], S[1]), pack2(S[2], S[3]), pack2(S[4], S[5]), pack2(S[6], S[7]));
+      uint4 hi, lo;
+      uint32_t *ph = &hi.x, *pl = &lo.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint64_t f = pair2(S[2 * i], S[2 * i + 1]);
+        ph[i] = take2(f);
+        pl[i] = pack2(f);
+      }
+      *reinterpret_cast<uint4*>(s) = hi;
+      *reinterpret_cast<uint4*>(s + LO) = lo;
       if (c > last || !local) continue;   // behind the end: no tokens
       const Factor f = c == last ? part : whole;
       const float l[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
@@ -268,12 +280,13 @@ __global__ void __launch_bounds__(128) lin_tc_scan_kernel(const __grid_constant_
 // map
 // ---------------------------------------------------------------------------
 // One CTA per 128 output rows: warps 0-3 hold a row per thread, one thread of warp 4 issues copies and products.
-//   O = a X, scaled row by row by lam^e(i); then per tile of 128 tokens S = a b^T, P = bf16(S * decay) written over
-//   S in tensor memory, O += P c.
+//   O = a X, scaled row by row by lam^e(i); then per tile of 128 tokens S = a b^T, P = S * decay as two bf16 terms
+//   written over S in tensor memory, O += P c.
 // S and O take 256 columns of tensor memory and a, b, c 96 KB of shared memory, so two CTAs share an SM and one's
-// products run under the other's decays; X passes through c's buffer before c's first tile.  What was tried against
-// it: one persistent CTA with two lanes of 128 rows, copies fetched ahead and separate warps for the outputs, whose
-// larger code ran at the same speed (a fifth of the cycles waiting for instructions).
+// products run under the other's decays; before their own tiles, X's first term passes through c's buffer and, once the
+// first scores have read b, its second through b's.  What was tried against it: one persistent CTA with two lanes of 128
+// rows, copies fetched ahead and separate warps for the outputs, whose larger code ran at the same speed (a fifth of the
+// cycles waiting for instructions).
 constexpr int kMapThreads = 160;
 template <int D> struct MapSmem {
   static constexpr int tile = TM * D * 2, panel = TM * 128;
@@ -284,12 +297,12 @@ template <int D> struct MapSmem {
 struct MapMaps { CUtensorMap a, b, c, out; };
 struct MapMapSets { MapMaps set[3]; };
 
-// P of one group of 32 columns: s * factor(row, group) * col[cc], or on the diagonal block s * lam^|i-j|.
+// The map's 128 rows of tile `tile`; REV: columns behind the rows instead of before them.
 template <int D, bool REV>
 __device__ __forceinline__ void map_tile(const MapMaps& maps, const LinMapArgs& a, int tile, uint32_t* status) {
   using L = MapSmem<D>;
   extern __shared__ uint8_t dyn[];
-  __shared__ uint64_t bar_a, full_b, full_c, bar_s, bar_o, bar_p;
+  __shared__ uint64_t bar_a, full_b, full_c, bar_s, bar_x, bar_o, bar_p;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_slot;
   __shared__ float diag[64];                // lam^n at 32 + n, zeros below
@@ -319,6 +332,7 @@ __device__ __forceinline__ void map_tile(const MapMaps& maps, const LinMapArgs& 
     mbar_init(&full_b, 1);
     mbar_init(&full_c, 1);
     mbar_init(&bar_s, 1);
+    mbar_init(&bar_x, 1);
     mbar_init(&bar_o, 1);
     mbar_init(&bar_p, 128);
     abort_slot = 0;
@@ -343,9 +357,10 @@ __device__ __forceinline__ void map_tile(const MapMaps& maps, const LinMapArgs& 
       int nb = 0, nc = 0;   // loads issued into b's and c's buffers
       load(as, &maps.a, i0, &bar_a);
       load(bs, &maps.b, j_first, &full_b);
+      const uint8_t* X = reinterpret_cast<const uint8_t*>(a.states + (((int64_t)b * a.H + h) * a.n_seg + seg) * D * D);
       if (has_state) {
         mbar_arrive_expect_tx(&full_c, D * D * 2);
-        bulk_g2s(cs, a.states + (((int64_t)b * a.H + h) * a.n_seg + seg) * D * D, D * D * 2, &full_c);
+        bulk_g2s(cs, X, D * D * 2, &full_c);
       } else {
         load(cs, &maps.c, j_first, &full_c);
       }
@@ -368,34 +383,51 @@ __device__ __forceinline__ void map_tile(const MapMaps& maps, const LinMapArgs& 
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) mma_ss(tm_s, da + kstep(k, L::panel), db + kstep(k, L::panel), id_s, k > 0);
         mma_commit(&bar_s);
-        if (t == 0 && has_state) {
-          ok = wait_or_abort(&full_c, 0, abort_flag);
-          if (!ok) break;
-          // X as stored has a's channel along rows; transposed, along columns
+        // X as stored has a's channel along rows; transposed, along columns
+        auto state_product = [&](uint32_t x, bool first) {
           const uint32_t id = idesc_bf16(128, D, false, !a.transposed);
-          const uint64_t dx = a.transposed ? kdesc0(sc) : mdesc0(sc, D * 128);
+          const uint64_t dx = a.transposed ? kdesc0(x) : mdesc0(x, D * 128);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(tm_o, da + kstep(k, L::panel), dx + (a.transposed ? kstep(k, D * 128) : mstep(k)), id, k > 0);
-          mma_commit(&bar_o);
+            mma_ss(tm_o, da + kstep(k, L::panel), dx + (a.transposed ? kstep(k, D * 128) : mstep(k)), id, !first || k > 0);
+        };
+        const bool state = t == 0 && has_state;
+        if (state) {   // X's first term, in c's buffer
+          ok = wait_or_abort(&full_c, 0, abort_flag);
+          if (!ok) break;
+          state_product(sc, true);
+          mma_commit(&bar_x);
         }
         ok = wait_or_abort(&bar_s, t & 1, abort_flag);
         if (!ok) break;
-        if (t + 1 < n_tiles) {
-          load(bs, &maps.b, j_first + (t + 1) * TM, &full_b);
+        if (state) {   // its second, through b's
+          mbar_arrive_expect_tx(&full_b, D * D * 2);
+          bulk_g2s(bs, X + D * D * 2, D * D * 2, &full_b);
           ++nb;
-        }
-        if (t == 0 && has_state) {
-          ok = wait_or_abort(&bar_o, no++ & 1, abort_flag);
+          ok = wait_or_abort(&bar_x, 0, abort_flag);
           if (!ok) break;
           load(cs, &maps.c, j_first, &full_c);
           ++nc;
+          ok = wait_or_abort(&full_b, (nb - 1) & 1, abort_flag);
+          if (!ok) break;
+          state_product(sb, false);
+          mma_commit(&bar_o);
+          ok = wait_or_abort(&bar_o, no++ & 1, abort_flag);
+          if (!ok) break;
+        }
+        if (t + 1 < n_tiles) {
+          load(bs, &maps.b, j_first + (t + 1) * TM, &full_b);
+          ++nb;
         }
         ok = wait_or_abort(&bar_p, t & 1, abort_flag) && wait_or_abort(&full_c, (nc - 1) & 1, abort_flag);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
-        for (int k = 0; k < TM / 16; ++k) mma_ts(tm_o, tm_s + 8 * k, dc + mstep(k), id_o, has_state || t || k);
+        for (int k = 0; k < TM / 16; ++k) {   // P's terms: 16 columns each of a group of 32 tokens
+          const uint32_t p = tm_s + 32 * (k >> 1) + 8 * (k & 1);
+          mma_ts(tm_o, p + 16, dc + mstep(k), id_o, has_state || t || k);
+          mma_ts(tm_o, p, dc + mstep(k), id_o, 1u);
+        }
         mma_commit(&bar_o);
       }
       if (!ok) {   // copies in flight end before the CTA does
@@ -422,38 +454,42 @@ __device__ __forceinline__ void map_tile(const MapMaps& maps, const LinMapArgs& 
       const int m = REV ? t : n_tiles - 1 - t;   // tiles between the rows and the columns
       const int n_valid = to_end - t * TM;       // columns within the sequence (below TM at its end only)
 #pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < 4; ++g) {   // P of 32 columns: s * factor(row, group) * col[cc]; on the diagonal block s * lam^|i-j|
         const int ahead = 4 * m + (REV ? g - warp : warp - g);   // groups from column to row
-        float s[32], p[16];
+        float s[32];
+        uint32_t p[32];   // the first terms of 32 columns, the second terms
         tmem_ld32(tm_s + lanes + 32 * g, s);
         tmem_wait_ld();
+        auto put = [&](int i, uint64_t f) {
+          p[i] = take2(f);
+          p[16 + i] = pack2(f);
+        };
         if (ahead > 0) {
           const float f = rowf * power32[ahead - 1];
           const uint64_t ff = pair2(f, f);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            p[i] = __uint_as_float(pack2(mul2(pair2(s[2 * i], s[2 * i + 1]), mul2(ff, col[i]))));
+          for (int i = 0; i < 16; ++i) put(i, mul2(pair2(s[2 * i], s[2 * i + 1]), mul2(ff, col[i])));
         } else if (ahead == 0) {
           const float* d = diag + 32 + (REV ? -lane : lane);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {   // zeros of the table for columns that the row does not see
             const float u = s[2 * i] * d[REV ? 2 * i : -2 * i], v = s[2 * i + 1] * d[REV ? 2 * i + 1 : -2 * i - 1];
-            p[i] = __uint_as_float(pack2((REV ? 2 * i >= lane : 2 * i <= lane) ? u : 0.f,
-                                         (REV ? 2 * i + 1 >= lane : 2 * i + 1 <= lane) ? v : 0.f));
+            put(i, pair2((REV ? 2 * i >= lane : 2 * i <= lane) ? u : 0.f, (REV ? 2 * i + 1 >= lane : 2 * i + 1 <= lane) ? v : 0.f));
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] = 0.f;
+          for (int i = 0; i < 32; ++i) p[i] = 0;
         }
         if (n_valid < TM) {   // columns behind the end, whatever their scores
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int c = 32 * g + 2 * i;
             const uint32_t keep = (c < n_valid ? 0xffffu : 0u) | (c + 1 < n_valid ? 0xffff0000u : 0u);
-            p[i] = __uint_as_float(__float_as_uint(p[i]) & keep);
+            p[i] &= keep;
+            p[16 + i] &= keep;
           }
         }
-        tmem_st16(tm_s + lanes + 16 * g, p);
+        tmem_st32(tm_s + lanes + 32 * g, p);
       }
       if (t == 0 && has_state) {   // O = a X, row by row lam^e(i) of it, before the tiles are added
         const float w = decay_pow(ld, REV ? max((int64_t)0, end - 1 - (i0 + row)) : i0 + row - s0 + 1);

@@ -63,3 +63,48 @@ def test_items_that_end_in_a_segments_first_tile(kda, d):
     M = ops.linear_bwd(*(clean[i].abs() for i in "qkv"), x["ld"], clean["d_o"].abs(), lengths, x["S0"].abs(), x["dSN"].abs())
     for name, g, r, m in zip(("dq", "dk", "dv", "dS0"), run_bwd(kda, x, lengths), ref, M):
         close(g, r, m, c if name != "dS0" else C32, name)
+
+
+def rounded(ref):
+    """What one rounding of the exact outputs to bf16 is off by, as a norm."""
+    return float((ref.to(torch.bfloat16).double() - ref).norm())
+
+
+def check_only_the_outputs_are_rounded(got, ref, M, what):
+    """Scores and states enter their products as two bf16 terms, which leaves 2^-16 of each; with the additions' 2^-16
+    of the sum over absolute values (C32) an element is within u |ref| + 3 x 2^-16 M.  The output's own rounding is
+    the rest: the error's norm is that of rounding the exact outputs, and at most 3 x 2^-16 of M's beside it."""
+    close(got, ref, M, 2 * 2.0 ** -16 + C32, what)
+    err = float((got.double() - ref).norm())
+    assert err <= rounded(ref) + 3 * 2.0 ** -16 * float(M.norm()), (what, err / rounded(ref))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,N,H", [(1, 384, 4), (2, 777, 3)])
+def test_outputs_of_bf16_problems_are_rounded_once(kda, B, N, H, d):
+    x = lin_inputs(23, B, N, H, d, torch.bfloat16)
+    o, SN, _ = run_fwd(kda, x)
+    ref = ops.linear_fwd(x["q"], x["k"], x["v"], x["ld"], None, x["S0"])
+    M = ops.linear_fwd(*(x[i].abs() for i in "qkv"), x["ld"], None, x["S0"].abs())
+    check_only_the_outputs_are_rounded(o, ref[0], M[0], "o")
+    ref = ops.linear_bwd(x["q"], x["k"], x["v"], x["ld"], x["d_o"], None, x["S0"], x["dSN"])
+    M = ops.linear_bwd(*(x[i].abs() for i in "qkv"), x["ld"], x["d_o"].abs(), None, x["S0"].abs(), x["dSN"].abs())
+    for name, g, r, m in zip(("dq", "dk", "dv"), run_bwd(kda, x), ref, M):
+        check_only_the_outputs_are_rounded(g, r, m, name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_token_through_the_pass_and_through_the_step(kda, d):
+    """The next token of a state through kda_linear_fwd and kda_linear_step: both from the fp32 state, each rounded once."""
+    B, H = 5, 7
+    x = lin_inputs(24, B, 1, H, d, torch.bfloat16)
+    o, SN, _ = run_fwd(kda, x)
+    p = kda.problem(B, H, d, 1, (0, 0, 0))
+    o1, S1 = torch.empty_like(o), torch.empty_like(SN)
+    kda.kda_linear_step(p, x["q"], x["k"], x["v"], x["ld"], x["S0"], o1, S1)
+    M, MS = ops.linear_fwd(*(x[i].abs() for i in "qkv"), x["ld"], None, x["S0"].abs())
+    # two roundings of values at most 4 x 2^-16 M apart: half a step each, 2^-8 of the larger
+    apart = (o.double() - o1.double()).abs()
+    assert (apart <= 2.0 ** -8 * (o.double().abs() + o1.double().abs()) + 4 * 2.0 ** -16 * M).all()
+    assert float((apart > 4 * 2.0 ** -16 * M).double().mean()) < 0.05   # most do not straddle a border
+    assert ((SN.double() - S1.double()).abs() <= 2 * C32 * MS).all()
