@@ -300,7 +300,7 @@ int kda_layernorm_bwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* d
  * lengths: [B] int32 or NULL (N each).  Item b's sequence is its first lengths[b] tokens (clamped to 0..N): what
  * q, k, v hold behind them is not used, whatever it is, o is zero there, and final_state is the state after the
  * item's own last token.  Inputs within the sequences must be finite.
- * The recurrence is evaluated in segments of 128 to 512 tokens on the tensor cores.  Of a bf16 problem the outputs alone
+ * The recurrence is evaluated in segments of 128 or 256 tokens on the tensor cores.  Of a bf16 problem the outputs alone
  * are rounded to bf16: decayed scores, and the states that enter segments, go into their products as two bf16 terms
  * (2^-16 of each is left out); the states themselves and final_state keep fp32 accuracy.  fp32 problems keep it
  * throughout.  The workspace is

@@ -27,7 +27,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kMaxSeg = 512;   // tokens per segment, at most; always a multiple of TM
+constexpr int kMaxSeg = 256;   // tokens per segment, at most; always a multiple of TM
 constexpr int TM = 128;       // tokens per tile of the map
 constexpr int TL = 64;        // tokens per tile of the local sums
 
@@ -617,12 +617,13 @@ cudaError_t map(const Dims& d, const LinMapSets& a, uint32_t* status, cudaStream
 
 }  // namespace
 
-// Tokens per segment.  A longer one costs the map more tiles of scores per row, a shorter one costs states: 189,272
-// tokens x 16 x 128 take 1.38 ms with 256, 1.32 with 512 and 1.52 with 1024; 4 x 8192 x 16 x 64, whose states are a
-// quarter as large, 145 us with 256 and 159 with 512.  Where the segments would not give every SM its two CTAs of the
-// local sums, shorter ones take less time in a row.
+// Tokens per segment.  A longer one costs the map more tiles of scores per row, a shorter one costs states.  33,272
+// tokens x 16 x 128: forward 296 us with 256, 292 with 512, 353 with 1024; backward 684, 714 and 930.  8 ragged prompts of
+// up to 2000: 128 us with 256 and 123 with 512, their backward pass 281 and 284; 4 x 8192 x 16 x 64: 169 us with 256 and 188 with
+// 512, backward 467 and 540.
+// Where the segments would not give every SM its two CTAs of the local sums, shorter ones take less time in a row.
 int linear_tc_segment(const Dims& d) {
-  int seg = d.dk == 128 ? kMaxSeg : kMaxSeg / 2;
+  int seg = kMaxSeg;
   while (seg > TM && (int64_t)d.B * d.H * ((d.N + seg - 1) / seg) < 2 * 148) seg /= 2;
   return seg;
 }
