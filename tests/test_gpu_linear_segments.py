@@ -26,7 +26,7 @@ def ragged(seed, n, N, H, d, dtype=torch.bfloat16):
     return x, torch.tensor(n, dtype=torch.int32, device="cuda")
 
 
-# few heads: segments of 128 tokens; many: of 512 (d = 128) and 256 (d = 64)
+# few heads: segments of 128 tokens; many: longer ones
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("n,H", [([1, 100, 129, 150, 385, 513, 897, 900], 3),
                                  ([1, 17, 127, 257, 260, 383, 513, 514, 530, 600, 639, 769, 770, 895, 1025, 1026, 1060, 1099, 1100], 16)])
@@ -108,3 +108,44 @@ def test_one_token_through_the_pass_and_through_the_step(kda, d):
     assert (apart <= 2.0 ** -8 * (o.double().abs() + o1.double().abs()) + 4 * 2.0 ** -16 * M).all()
     assert float((apart > 4 * 2.0 ** -16 * M).double().mean()) < 0.05   # most do not straddle a border
     assert ((SN.double() - S1.double()).abs() <= 2 * C32 * MS).all()
+
+
+def tokens_per_segment(kda, x, lengths):
+    """The segment that a bf16 problem is cut into, from how far its pass writes into the workspace: 4 d^2 bytes per
+    item, head and segment behind the first 256."""
+    B, N, H, d = x["q"].shape
+    ws = kda.alloc_linear_workspace(kda.problem(B, H, d, N, (0, 0, 0)), torch.bfloat16)
+    marks = ws[: ws.numel() // 4 * 4].view(torch.int32)
+    marks.fill_(0x5a5a5a5a)
+    run_fwd(kda, x, lengths, ws=ws)
+    states = -(-(int((marks != 0x5a5a5a5a).nonzero()[-1]) + 1 - 64) // (d * d))
+    assert states % (B * H) == 0
+    return next(s for s in (128, 256, 512, 1024) if -(-N // s) == states // (B * H))
+
+
+ENDS = [0, 1, 63, 64, 65, 127, 128, 129, 191, 193, 255, 256, 257, 383, 385, 511, 513, 900, 1100]
+
+
+@pytest.mark.parametrize("state", [True, False])
+@pytest.mark.parametrize("d,H", [(64, 15), (128, 16)])
+def test_long_segments(kda, d, H, state):
+    """Segments of several tiles against the recurrence: nothing forgotten, far tokens, ragged ends in every tile, NaN
+    behind them.  Enough items and heads for the longest segments, which the test asks for."""
+    x, lengths = ragged(25, ENDS, 1100, H, d)
+    x["ld"][:6] = torch.tensor([0.0, -1e-3, -1e-6, -0.02, -4.0, -float("inf")])
+    assert tokens_per_segment(kda, x, lengths) == 256
+    clean = dict(x, **{i: ops._until(x[i], lengths) for i in ("q", "k", "v", "d_o")})
+    S0, dSN = (x["S0"], x["dSN"]) if state else (None, None)
+    size = lambda t: None if t is None else t.abs()   # noqa: E731
+    o, SN, _ = run_fwd(kda, x, lengths, state)
+    ref = ops.linear_fwd(*(clean[i] for i in "qkv"), x["ld"], lengths, S0)
+    M = ops.linear_fwd(*(clean[i].abs() for i in "qkv"), x["ld"], lengths, size(S0))
+    check_only_the_outputs_are_rounded(o, ref[0], M[0], "o")
+    close(SN, ref[1], M[1], C32, "final state")
+    ref = ops.linear_bwd(*(clean[i] for i in "qkv"), x["ld"], clean["d_o"], lengths, S0, dSN)
+    M = ops.linear_bwd(*(clean[i].abs() for i in "qkv"), x["ld"], clean["d_o"].abs(), lengths, size(S0), size(dSN))
+    for name, g, r, m in zip(("dq", "dk", "dv", "dS0"), run_bwd(kda, x, lengths, state), ref, M):
+        if name == "dS0":
+            close(g, r, m, C32, name)
+        else:
+            check_only_the_outputs_are_rounded(g, r, m, name)
