@@ -265,8 +265,8 @@ typedef struct {
  * inv_freq: [d/2] fp32 device values.  positions: [B, N, 3] int32 (time, height, width; any sign), or NULL for
  * the positions of the token stream: text token i at (i, i, i), visual token (t, h, w) at (text_len + t,
  * text_len + h, text_len + w).  Angles are reduced in fp64, so far positions keep the accuracy of near ones.
- * k and k_out may both be NULL (one tensor only).  Works in place with q_out = q, k_out = k (exactly).
- * Returns a kda_status. */
+ * k and k_out may both be NULL (one tensor only).  Works in place with q_out = q, k_out = k (exactly; where q and k
+ * are one tensor, neither output may be it).  Returns a kda_status. */
 int kda_rope_fwd(const kda_problem* p, const kda_rope* rope, kda_dtype dtype,
                  const void* q, const void* k, const float* inv_freq, const int32_t* positions,
                  void* q_out, void* k_out, void* stream);

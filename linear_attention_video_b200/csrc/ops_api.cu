@@ -31,14 +31,16 @@ bool overlap(const Span& a, const Span& b) {
   return x < y + b.bytes && y < x + a.bytes;
 }
 
-// Outputs share no byte with an input or with one another.  `in_place` pairs (output i, its input) may be the same range.
-int check_alias(std::initializer_list<Span> outs, std::initializer_list<Span> ins,
-                std::initializer_list<const void*> in_place = {}) {
+// Outputs share no byte with an input or with one another.  Output i may be the same range as the input whose place in
+// `ins` in_place[i] gives (-1: none), and as that one alone: another argument at the same address is still read.
+int check_alias(std::initializer_list<Span> outs, std::initializer_list<Span> ins, std::initializer_list<int> in_place = {}) {
   int i = 0;
   for (const Span& o : outs) {
+    int j = 0;
     for (const Span& in : ins) {
-      const bool same = o.p == in.p && o.bytes == in.bytes && i < (int)in_place.size() && in_place.begin()[i] == in.p;
-      if (!same && overlap(o, in)) return KDA_ERR_INVALID_ARG;
+      const bool own = i < (int)in_place.size() && in_place.begin()[i] == j;
+      if (!(own && o.p == in.p && o.bytes == in.bytes) && overlap(o, in)) return KDA_ERR_INVALID_ARG;
+      ++j;
     }
     for (const Span* p = outs.begin(); p != &o; ++p)
       if (overlap(*p, o)) return KDA_ERR_INVALID_ARG;
@@ -88,7 +90,7 @@ int run_rope(const kda_problem* p, const kda_rope* r, kda_dtype dt, const void* 
   const size_t n = act_bytes(d, dt);
   const Span sq{q, n}, sk{k, n}, oq{qo, n}, ok{ko, n}, fr{inv_freq, (size_t)d.dk / 2 * 4}, ps{positions, (size_t)tokens * 12};
   if ((st = check_aligned({sq, oq, fr}, {sk, ok, ps}))) return st;
-  if ((st = check_alias({oq, ok}, {sq, sk, fr, ps}, {q, k}))) return st;
+  if ((st = check_alias({oq, ok}, {sq, sk, fr, ps}, {0, 1}))) return st;
   const kda::RopeArgs a{{q, k}, {qo, ko}, inv_freq, positions, tokens, d.N, d.L, d.H, d.Hg, d.Wg,
                         k ? 2 : 1, r->pairs_t, r->pairs_h, inverse};
   int launches = 0;
@@ -224,7 +226,7 @@ int kda_linear_step(const kda_problem* p, kda_dtype dtype, const void* q, const 
   const size_t n = act_bytes(d, dtype), m = one_state(d);
   const Span sq{q, n}, sk{k, n}, sv{v, n}, sl{log_decay, (size_t)d.H * 4}, si{state_in, m}, so{o, n}, su{state_out, m};
   if ((st = check_aligned({sq, sk, sv, sl, si, so, su}, {}))) return st;
-  if ((st = check_alias({so, su}, {sq, sk, sv, sl, si}, {nullptr, state_in}))) return st;
+  if ((st = check_alias({so, su}, {sq, sk, sv, sl, si}, {-1, 4}))) return st;
   int launches = 0;
   return finish(kda::launch_linear_step(d, dtype, {q, k, v, log_decay, state_in, o, state_out, d.H},
                                         static_cast<cudaStream_t>(stream), &launches), launches);

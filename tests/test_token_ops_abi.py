@@ -183,3 +183,19 @@ def test_binding_checks_tensors_before_the_call():
         kda.alloc_linear_workspace(_p(d=96), torch.float32)
     with pytest.raises(kda.KdaError):
         kda.kda_layernorm_fwd(torch.zeros(()), torch.zeros(()))
+
+
+@pytest.mark.parametrize("which", ["kda_rope_fwd", "kda_rope_bwd"])
+def test_rope_in_place_is_over_the_outputs_own_input_alone(which):
+    """One tensor as q and k: q_out over it would turn what k is still read from."""
+    p, r = _p(), kda.rope((4, 14, 14))
+    call = lambda **kw: _rope(p, r, which=which, **kw)   # noqa: E731
+    assert call(q=A, k=A, qo=A, ko=6 * A) == INVALID
+    assert call(q=A, k=A, qo=5 * A, ko=A) == INVALID
+    assert call(q=A, k=A, qo=A, ko=A) == INVALID
+    assert call(q=A, k=2 * A, qo=2 * A, ko=A) == INVALID           # over each other's
+
+
+def test_step_in_place_is_over_the_state_alone():
+    p = _p(text_len=1, grid=(0, 0, 0))
+    assert _step(p, q=5 * A, si=5 * A, so=5 * A) == INVALID        # q lies in the state
