@@ -287,7 +287,8 @@ int kda_layernorm_fwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* x
 
 /* Its backward pass: dx [rows, cols] of dtype from dy, x and the forward pass's mean and rstd, and the sums over
  * the rows d_weight, d_bias [cols] fp32 (either may be NULL).  The workspace is
- * kda_layernorm_bwd_workspace_bytes(rows, cols) bytes, 256-byte aligned.  Returns a kda_status. */
+ * kda_layernorm_bwd_workspace_bytes(rows, cols) bytes, 256-byte aligned; one that serves a problem serves every other with
+ * at most as many rows and columns.  Returns a kda_status. */
 size_t kda_layernorm_bwd_workspace_bytes(int64_t rows, int32_t cols);
 int kda_layernorm_bwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* dy, const void* x,
                       const float* weight, const float* mean, const float* rstd, void* dx, float* d_weight,
@@ -305,7 +306,8 @@ int kda_layernorm_bwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* d
  * (2^-16 of each is left out); the states themselves and final_state keep fp32 accuracy.  fp32 problems keep it
  * throughout.  The workspace is
  * kda_linear_workspace_bytes(p, dtype) bytes, 256-byte aligned (4 d^2 bytes per batch item, head and segment beside
- * the status word).  Returns a kda_status. */
+ * the status word); one that serves a problem serves every other of its dtype and d with at most as many tokens, and at
+ * most as many items times heads.  So does the backward pass's.  Returns a kda_status. */
 size_t kda_linear_workspace_bytes(const kda_problem* p, kda_dtype dtype);
 int kda_linear_fwd(const kda_problem* p, kda_dtype dtype,
                    const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,

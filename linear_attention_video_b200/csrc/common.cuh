@@ -163,6 +163,7 @@ cudaError_t launch_linear_bwd(const Dims& d, kda_dtype dt, const void* q, const 
                               uint32_t* status, cudaStream_t s, int* launches);
 // bf16 problems (linear_tc.cu); the states between the launches are operand images (see there).
 int linear_tc_segment(const Dims& d);
+int64_t linear_tc_most_states(const Dims& d);
 cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalSets& a, uint32_t* status, cudaStream_t s);
 cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanSets& a, cudaStream_t s);
 cudaError_t launch_linear_tc_map(const Dims& d, const LinMapSets& a, uint32_t* status, cudaStream_t s);

@@ -517,8 +517,12 @@ cudaError_t launch_norm_fwd(const NormFwdArgs& a, kda_dtype dt, cudaStream_t s, 
   return e;
 }
 
+// What no problem with fewer rows or columns exceeds: the grid shrinks behind 2048 and 4096 columns alone.
 size_t norm_bwd_parts(int64_t rows, int cols) {
-  return (size_t)bwd_grid(rows, cols) * 2 * cols * sizeof(float);
+  size_t most = (size_t)bwd_grid(rows, cols) * cols;
+  for (int c : {2048, 4096})
+    if (c < cols) most = std::max(most, (size_t)bwd_grid(rows, c) * c);
+  return most * 2 * sizeof(float);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, kda_dtype dt, float* dw, float* db, cudaStream_t s, int* launches) {

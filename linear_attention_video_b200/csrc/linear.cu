@@ -200,7 +200,9 @@ struct Pass {
   }
 };
 
+// Of the states between the launches, for every problem up to this one's size.
 size_t state_bytes(const Dims& d, kda_dtype dt) {
+  if (dt == KDA_DT_BF16) return (size_t)linear_tc_most_states(d) * d.dk * d.dv * sizeof(float);
   return Pass(d, dt, nullptr, nullptr, nullptr, nullptr, nullptr).state_floats() * sizeof(float);
 }
 

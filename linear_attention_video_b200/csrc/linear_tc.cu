@@ -627,6 +627,13 @@ int linear_tc_segment(const Dims& d) {
   while (seg > TM && (int64_t)d.B * d.H * ((d.N + seg - 1) / seg) < 2 * 148) seg /= 2;
   return seg;
 }
+// States that a workspace holds: what no problem with fewer items, heads or tokens exceeds.  A halved segment means
+// fewer than 2 x 148 of the longer ones, so at most twice as many less two.
+int64_t linear_tc_most_states(const Dims& d) {
+  static_assert(kMaxSeg == 2 * TM, "one halving");
+  const int64_t pairs = (int64_t)d.B * d.H, whole = pairs * ((d.N + kMaxSeg - 1) / kMaxSeg), halves = pairs * ((d.N + TM - 1) / TM);
+  return std::max(whole, std::min<int64_t>(halves, 2 * (2 * 148 - 1)));
+}
 
 cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalSets& a, uint32_t* status, cudaStream_t s) {
   return d.dk == 128 ? local<128>(d, a, status, s) : local<64>(d, a, status, s);

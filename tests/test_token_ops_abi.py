@@ -199,3 +199,27 @@ def test_rope_in_place_is_over_the_outputs_own_input_alone(which):
 def test_step_in_place_is_over_the_state_alone():
     p = _p(text_len=1, grid=(0, 0, 0))
     assert _step(p, q=5 * A, si=5 * A, so=5 * A) == INVALID        # q lies in the state
+
+
+def test_linear_workspace_sizes_never_fall_as_the_problem_grows():
+    """A workspace for the largest problem serves every smaller one: fewer items, heads or tokens never need more."""
+    N = [1, 2, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1000, 2048, 2500, 4096, 4608, 4609, 5000, 9216, 10000, 18944, 20000, 40000, 189272]
+    pairs = [(1, 1), (1, 2), (1, 3), (1, 8), (1, 13), (1, 16), (2, 16), (3, 16), (9, 16), (10, 15), (19, 16), (37, 16), (64, 24)]
+    for size in (kda.kda_linear_workspace_bytes, kda.kda_linear_bwd_workspace_bytes):
+        for dtype in (torch.bfloat16, torch.float32):
+            for d in (64, 128):
+                at = [[size(kda.problem(B, H, d, n, (0, 0, 0)), dtype) for n in N] for B, H in pairs]
+                for (B, H), row in zip(pairs, at):
+                    assert row == sorted(row) and row[0] > 256, (d, dtype, B, H)
+                for n, col in zip(N, zip(*at)):   # by items x heads
+                    assert sorted(col) == [s for _, s in sorted((B * H, s) for (B, H), s in zip(pairs, col))], (d, dtype, n)
+
+
+def test_layernorm_workspace_sizes_never_fall_as_the_problem_grows():
+    rows = [0, 1, 2, 15, 16, 147, 148, 149, 295, 296, 297, 591, 592, 593, 5000, 100000]
+    cols = [1, 7, 16, 127, 128, 129, 256, 257, 1024, 1025, 2047, 2048, 2049, 3000, 4095, 4096, 4097, 5001, 8192, 8193, 16384]
+    at = [[kda.kda_layernorm_bwd_workspace_bytes(r, c) for c in cols] for r in rows]
+    for r, row in zip(rows, at):
+        assert row == sorted(row), r
+    for c, col in zip(cols, zip(*at)):
+        assert list(col) == sorted(col), c
