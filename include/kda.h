@@ -288,7 +288,7 @@ int kda_layernorm_fwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* x
 /* Its backward pass: dx [rows, cols] of dtype from dy, x and the forward pass's mean and rstd, and the sums over
  * the rows d_weight, d_bias [cols] fp32 (either may be NULL).  The workspace is
  * kda_layernorm_bwd_workspace_bytes(rows, cols) bytes, 256-byte aligned; one that serves a problem serves every other with
- * at most as many rows and columns.  Returns a kda_status. */
+ * at most as many rows and columns.  A call without rows leaves it as it is, its status word too.  Returns a kda_status. */
 size_t kda_layernorm_bwd_workspace_bytes(int64_t rows, int32_t cols);
 int kda_layernorm_bwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* dy, const void* x,
                       const float* weight, const float* mean, const float* rstd, void* dx, float* d_weight,

@@ -107,7 +107,8 @@ struct NormBwdArgs {
 };
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, kda_dtype dt, cudaStream_t s, int* launches);
 size_t norm_bwd_parts(int64_t rows, int cols);
-cudaError_t launch_norm_bwd(const NormBwdArgs& a, kda_dtype dt, float* dw, float* db, cudaStream_t s, int* launches);
+// The pass has no condition to record: it clears `status`.
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, kda_dtype dt, float* dw, float* db, uint32_t* status, cudaStream_t s, int* launches);
 
 // Linear attention with a decay per head (linear.cu).
 struct LinLocalArgs {

@@ -414,7 +414,8 @@ __global__ void __launch_bounds__(Shape<G>::threads, ctas_of(Shape<G>::threads, 
 }
 
 // Adds the partials of 32 columns: 32 strands of rows, joined in a fixed order.
-__global__ void __launch_bounds__(1024) norm_sum_kernel(const float* parts, int n_parts, int cols, float* dw, float* db) {
+__global__ void __launch_bounds__(1024) norm_sum_kernel(const float* parts, int n_parts, int cols, float* dw, float* db, uint32_t* status) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   __shared__ float sm[32][33];
   const int cx = threadIdx.x % 32, ry = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + cx;   // over 2 * cols: the weight's sums, then the bias's
@@ -525,7 +526,7 @@ size_t norm_bwd_parts(int64_t rows, int cols) {
   return most * 2 * sizeof(float);
 }
 
-cudaError_t launch_norm_bwd(const NormBwdArgs& a, kda_dtype dt, float* dw, float* db, cudaStream_t s, int* launches) {
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, kda_dtype dt, float* dw, float* db, uint32_t* status, cudaStream_t s, int* launches) {
   cudaError_t e;
   if (a.rows == 0) {   // no rows: the sums are zero
     if (dw && (e = cudaMemsetAsync(dw, 0, (size_t)a.cols * sizeof(float), s)) != cudaSuccess) return e;
@@ -537,8 +538,8 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& a, kda_dtype dt, float* dw, float
   else e = a.cols % 4 == 0 ? bwd<float, 4>(a, grid, s) : bwd<float, 1>(a, grid, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
-  if (!dw && !db) return cudaSuccess;
-  norm_sum_kernel<<<(2 * a.cols + 31) / 32, 1024, 0, s>>>(a.parts, grid, a.cols, dw, db);
+  if (!dw && !db) return cudaMemsetAsync(status, 0, sizeof(uint32_t), s);
+  norm_sum_kernel<<<(2 * a.cols + 31) / 32, 1024, 0, s>>>(a.parts, grid, a.cols, dw, db, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   *launches += 1;
   return cudaSuccess;

@@ -155,8 +155,8 @@ int kda_layernorm_bwd(int64_t rows, int32_t cols, kda_dtype dtype, const void* d
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* parts = d_weight || d_bias ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes) : nullptr;
   int launches = 0;
-  return finish(kda::launch_norm_bwd({dy, x, weight, mean, rstd, dx, parts, rows, cols}, dtype, d_weight, d_bias, s,
-                                     &launches), launches);
+  return finish(kda::launch_norm_bwd({dy, x, weight, mean, rstd, dx, parts, rows, cols}, dtype, d_weight, d_bias,
+                                     static_cast<uint32_t*>(workspace), s, &launches), launches);
 }
 
 size_t kda_linear_workspace_bytes(const kda_problem* p, kda_dtype dtype) {

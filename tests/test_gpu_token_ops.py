@@ -451,3 +451,12 @@ def test_layernorm_many_rows(kda):
     _, rw, rb = ops.layernorm_bwd(dy, x, mean, rstd)
     assert float((dw.double() - rw).norm() / rw.norm()) < TOL_F32_REL_L2
     assert float((db.double() - rb).norm() / rb.norm()) < TOL_F32_REL_L2
+
+
+def test_layernorm_backward_workspace_has_a_status(kda):
+    """Whatever stood in the workspace before."""
+    x, dy = randn(gen(78), 37, 257), randn(gen(79), 37, 257)
+    for sums in (None, torch.empty(257, device="cuda")):
+        ws = kda.alloc_layernorm_bwd_workspace(37, 257).fill_(0xff)
+        kda.kda_layernorm_bwd(dy, x, x.mean(1), x.std(1).reciprocal(), torch.empty_like(x), ws, None, sums)
+        assert kda.kda_read_status(ws) == kda.KDA_OK
