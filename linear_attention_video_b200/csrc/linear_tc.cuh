@@ -49,9 +49,13 @@ __device__ __forceinline__ uint32_t pack2(uint64_t ab) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
   return pack2(a, b);
 }
-// ab = bf16 pair + the rest
+// ab = bf16 pair + the rest.  A value above the largest bf16 one takes that one (rounded to nearest it would be infinite,
+// and the rest with it): the rest is below 2^-8 of it either way.
 __device__ __forceinline__ uint32_t take2(uint64_t& ab) {
-  const uint32_t v = pack2(ab);
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+  uint32_t v;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(b), "f"(a));
   ab = sub2(ab, wide2(v));
   return v;
 }

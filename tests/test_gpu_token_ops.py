@@ -460,3 +460,34 @@ def test_layernorm_backward_workspace_has_a_status(kda):
         ws = kda.alloc_layernorm_bwd_workspace(37, 257).fill_(0xff)
         kda.kda_layernorm_bwd(dy, x, x.mean(1), x.std(1).reciprocal(), torch.empty_like(x), ws, None, sums)
         assert kda.kda_read_status(ws) == kda.KDA_OK
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_linear_values_beside_the_largest(kda, d):
+    """fp32 values above the largest bf16 one, 3.39e38, in the inputs and in a state: their first bf16 term may not be
+    infinite.  Sums and products stay in range."""
+    top = torch.finfo(torch.float32).max
+    for dtype in (torch.float32, torch.bfloat16):
+        x = lin_inputs(17, 1, 300, 2, d, torch.float32)
+        x["S0"] = torch.where(x["S0"] > 1.0, top, x["S0"].sign() * 1e36)
+        x["dSN"] *= 1e-30
+        if dtype == torch.float32:
+            x["v"] = torch.where(x["v"] > 1.0, top, x["v"] * 1e36)
+        x["q"], x["k"], x["d_o"] = x["q"] * 1e-6, x["k"] * 1e-12, x["d_o"] * 1e-30
+        x = {n: t.to(dtype) if n in ("q", "k", "v", "d_o") else t for n, t in x.items()}
+        o, SN, ws = run_fwd(kda, x)
+        ref = ops.linear_fwd(x["q"], x["k"], x["v"], x["ld"], None, x["S0"])
+        M = ops.linear_fwd(*(x[n].abs() for n in "qkv"), x["ld"], None, x["S0"].abs())
+        assert torch.isfinite(ref[0].float()).all() and torch.isfinite(ref[1].float()).all()
+        c = C32 + (2.0 ** -8 if dtype == torch.bfloat16 else 0.0)
+        close(o, ref[0], M[0], c, "o")
+        close(SN, ref[1], M[1], C32, "final state")
+        ref = ops.linear_bwd(x["q"], x["k"], x["v"], x["ld"], x["d_o"], None, x["S0"], x["dSN"])
+        M = ops.linear_bwd(*(x[n].abs() for n in "qkv"), x["ld"], x["d_o"].abs(), None, x["S0"].abs(), x["dSN"].abs())
+        for name, g, r, m in zip(("dq", "dk", "dv", "dS0"), run_bwd(kda, x), ref, M):
+            if name == "dv":
+                # k dSN and k (q do) are of 1e-12 x 1e-30: all of it lies below the smallest normal number, 2^-126, where
+                # one step is 2^-149 (bf16: 2^-133), 1e-3 of it (all of it), and no relative bound can hold
+                assert float(m.max()) < 2.0 ** -126 and ((g.double() - r).abs() <= 2.0 ** -126).all()
+                continue
+            close(g, r, m, C32 if name == "dS0" else c, name)
