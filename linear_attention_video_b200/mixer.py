@@ -186,9 +186,11 @@ class LinearLayer:
         kda_linear_step(self.p1, q, k, v, self.log_decay, state, o, state)
         return o.view(self.B, 1, -1) @ self.wo
 
-    def backward(self, x, dy, lengths=None, positions=None):
-        """Gradients of sum(dy * self(x)): that of x, and a dict of the weights'.  The forward pass up to the
-        attention is computed again; nothing of it has to be kept.  Tokens behind an item's length change nothing."""
+    def backward(self, x, dy, lengths=None, positions=None, initial_state=None, d_final_state=None, d_initial_state=None):
+        """Gradients of sum(dy * self(x)) + sum(d_final_state * final state): that of x, and a dict of the weights'.
+        A sequence in pieces gives its piece's initial_state again and gets the gradient for the piece before in
+        d_initial_state (fp32 states [B, H, d, d], or None).  The forward pass up to the attention is computed again;
+        nothing of it has to be kept.  Tokens behind an item's length change nothing."""
         B, N, D = x.shape
         rows = B * N
         if lengths is not None:   # the weights' products run over all rows: 0 times what stands there has to be 0
@@ -197,13 +199,14 @@ class LinearLayer:
         mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
         h, q, k, v = self._qkv(self.p, x, positions, (mean, rstd))
         o = torch.empty_like(v)
-        kda_linear_fwd(self.p, q, k, v, self.log_decay, o, self.ws, lengths=lengths)
+        kda_linear_fwd(self.p, q, k, v, self.log_decay, o, self.ws, lengths=lengths, initial_state=initial_state)
         if self.ws_bwd is None:
             self.ws_bwd = (alloc_linear_bwd_workspace(self.p, x.dtype, x.device),
                            alloc_layernorm_bwd_workspace(rows, D, x.device))
         d_o = (dy @ self.wo.t()).view(B, N, self.H, self.d)
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        kda_linear_bwd(self.p, q, k, v, self.log_decay, d_o, dq, dk, dv, self.ws_bwd[0], lengths=lengths)
+        kda_linear_bwd(self.p, q, k, v, self.log_decay, d_o, dq, dk, dv, self.ws_bwd[0], lengths=lengths,
+                       initial_state=initial_state, d_final_state=d_final_state, d_initial_state=d_initial_state)
         kda_rope_bwd(self.p, self.rope, dq, dk, self.inv_freq, dq, dk, positions=positions)
         flat = lambda t: t.reshape(rows, D)   # noqa: E731
         grads = {"wo": flat(o).t() @ flat(dy), "wq": flat(h).t() @ flat(dq), "wk": flat(h).t() @ flat(dk),

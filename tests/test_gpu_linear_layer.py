@@ -137,3 +137,49 @@ def test_layer_captured_in_a_graph(layer):
     torch.cuda.synchronize()
     assert torch.equal(y, y2) and torch.equal(dx, dx2)
     assert torch.equal(grads["norm_w"], grads2["norm_w"]) and torch.equal(grads["norm_b"], grads2["norm_b"])
+
+
+def test_gradients_of_a_piece_between_carried_states(layer):
+    """A sequence in pieces: the state that enters, the gradient that comes back through the state that leaves, and the
+    gradient for the piece before, with items that end inside the piece."""
+    g = torch.Generator().manual_seed(8)
+    x, dy = _x(8), _x(9)
+    S0, dSN = (torch.randn(2, H, d, d, generator=g).cuda() for _ in range(2))
+    for n in (None, torch.tensor([N, 211], dtype=torch.int32, device="cuda")):
+        w = {k: t.requires_grad_(k not in ("log_decay", "inv_freq")) for k, t in weights(layer).items()}
+        x64, s64 = x.double().requires_grad_(), S0.double().requires_grad_()
+        y, SN = carried_reference(w, x64, s64, n)
+        final = torch.empty_like(S0)
+        assert rel(layer(x, lengths=n, initial_state=S0, final_state=final), y.detach()) <= FWD
+        assert rel(final, SN.detach()) <= FWD
+        ((y * dy.double()).sum() + (SN * dSN.double()).sum()).backward()
+        dS0 = torch.empty_like(S0)
+        dx, grads = layer.backward(x, dy, lengths=n, initial_state=S0, d_final_state=dSN, d_initial_state=dS0)
+        assert rel(dx, x64.grad) <= BWD, rel(dx, x64.grad)
+        assert rel(dS0, s64.grad) <= BWD, rel(dS0, s64.grad)
+        for name, t in grads.items():
+            assert rel(t, w[name].grad) <= BWD, (name, rel(t, w[name].grad))
+
+
+def carried_reference(w, x, S0, lengths=None):
+    """The layer in fp64 from a state, and the state behind each item's last token; differentiable."""
+    B, n, _ = x.shape
+    mean = x.mean(-1, keepdim=True)
+    h = (x - mean) / torch.sqrt(((x - mean) ** 2).mean(-1, keepdim=True) + 1e-5) * w["norm_w"] + w["norm_b"]
+    q, k, v = ((h @ w[i]).view(B, n, H, d) for i in ("wq", "wk", "wv"))
+    pos = ops.grid_positions(B, TEXT, GRID).to(x.device)
+    a = (pos.double()[..., torch.tensor([0] * 16 + [1] * 24 + [2] * 24, device=x.device)] * w["inv_freq"]).unsqueeze(2)
+    turn = lambda t: torch.cat([t[..., :64] * a.cos() - t[..., 64:] * a.sin(), t[..., :64] * a.sin() + t[..., 64:] * a.cos()], -1)   # noqa: E731
+    q, k = turn(q), turn(k)
+    i, ld = torch.arange(n, device=x.device), w["log_decay"].view(H, 1, 1)
+    last = torch.full((B,), n, device=x.device) if lengths is None else lengths.long()
+    live = (i.view(1, -1, 1, 1) < last.view(-1, 1, 1, 1)).double()
+    zero = torch.zeros((), dtype=torch.float64, device=x.device)
+    gap = i.view(-1, 1) - i
+    decay = torch.where(gap >= 0, torch.exp(ld * gap.clamp(min=0)), zero)
+    o = torch.einsum("bihc,bjhc,hij,bjhe->bihe", q, k, decay, v)
+    o = o + torch.einsum("hi,bihc,bhce->bihe", torch.exp(ld[..., 0] * (i + 1)), q, S0)
+    left = last.view(-1, 1, 1) - 1 - i                                            # [B, 1, n]
+    end = torch.where(left >= 0, torch.exp(ld.view(1, H, 1) * left.clamp(min=0)), zero)
+    SN = torch.einsum("bhj,bjhc,bjhe->bhce", end, k, v) + torch.exp(ld.view(1, H, 1, 1) * last.view(-1, 1, 1, 1)) * S0
+    return (o * live).reshape(B, n, D) @ w["wo"], SN
