@@ -493,18 +493,21 @@ cudaError_t bwd_shape(const NormBwdArgs& a, int grid, cudaStream_t s) {
 #undef KDA_NORM
   return cudaGetLastError();
 }
+// CTAs of lanes with e elements and r rows at a time: as many as are resident at once, no more than there are row groups.
+int bwd_grid(int64_t rows, int cols, int e, int r) {
+  const int g = lanes_for(cols, e), per = groups_for(g) * r;
+  return (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)148 * ctas_of(std::max(128, g), kBwdThreads));
+}
+bool narrow_scalar(int cols, int v) { return v == 1 && cols <= 8 * 512; }
+// Of accesses of v elements.
+int bwd_grid(int64_t rows, int cols, int v) {
+  return narrow_scalar(cols, v) ? bwd_grid(rows, cols, 8, 2) : bwd_grid(rows, cols, 16, 1);
+}
 template <typename T, int V>
 cudaError_t bwd(const NormBwdArgs& a, int grid, cudaStream_t s) {
   if constexpr (V == 1)
-    if (a.cols <= 8 * 512) return bwd_shape<T, V, 8, 2>(a, grid, s);
+    if (narrow_scalar(a.cols, V)) return bwd_shape<T, V, 8, 2>(a, grid, s);
   return bwd_shape<T, V, 16, 1>(a, grid, s);
-}
-
-// CTAs of the backward pass: enough to fill the GPU, no more than there are row groups.
-int bwd_grid(int64_t rows, int cols) {
-  // lanes for 16 elements each; scalar rows have twice as many lanes and rows per turn, so as many groups' rows
-  const int g = lanes_for(cols, 16), threads = std::max(128, g), per = groups_for(g);
-  return (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)148 * ctas_of(threads, kBwdThreads));
 }
 
 }  // namespace
@@ -518,11 +521,12 @@ cudaError_t launch_norm_fwd(const NormFwdArgs& a, kda_dtype dt, cudaStream_t s, 
   return e;
 }
 
-// What no problem with fewer rows or columns exceeds: the grid shrinks behind 2048 and 4096 columns alone.
+// What no problem with fewer rows or columns exceeds.  The shape of 16 elements has the larger grid of the two (the other
+// has as many or twice as many lanes and rows at a time), and its grid shrinks behind 2048 and 4096 columns alone.
 size_t norm_bwd_parts(int64_t rows, int cols) {
-  size_t most = (size_t)bwd_grid(rows, cols) * cols;
+  size_t most = (size_t)bwd_grid(rows, cols, 16, 1) * cols;
   for (int c : {2048, 4096})
-    if (c < cols) most = std::max(most, (size_t)bwd_grid(rows, c) * c);
+    if (c < cols) most = std::max(most, (size_t)bwd_grid(rows, c, 16, 1) * c);
   return most * 2 * sizeof(float);
 }
 
@@ -533,9 +537,10 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& a, kda_dtype dt, float* dw, float
     if (db && (e = cudaMemsetAsync(db, 0, (size_t)a.cols * sizeof(float), s)) != cudaSuccess) return e;
     return cudaSuccess;
   }
-  const int grid = bwd_grid(a.rows, a.cols);
-  if (dt == KDA_DT_BF16) e = a.cols % 8 == 0 ? bwd<__nv_bfloat16, 8>(a, grid, s) : bwd<__nv_bfloat16, 1>(a, grid, s);
-  else e = a.cols % 4 == 0 ? bwd<float, 4>(a, grid, s) : bwd<float, 1>(a, grid, s);
+  const int v = dt == KDA_DT_BF16 ? (a.cols % 8 == 0 ? 8 : 1) : (a.cols % 4 == 0 ? 4 : 1);
+  const int grid = bwd_grid(a.rows, a.cols, v);
+  if (dt == KDA_DT_BF16) e = v == 8 ? bwd<__nv_bfloat16, 8>(a, grid, s) : bwd<__nv_bfloat16, 1>(a, grid, s);
+  else e = v == 4 ? bwd<float, 4>(a, grid, s) : bwd<float, 1>(a, grid, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (!dw && !db) return cudaMemsetAsync(status, 0, sizeof(uint32_t), s);
