@@ -215,8 +215,9 @@ __global__ void __launch_bounds__(kLocalThreads, 2) lin_tc_local_kernel(const __
 // scan
 // ---------------------------------------------------------------------------
 // A thread takes 8 columns of one row: 32 bytes of the local state, 16 each of the two images over them.
-// U local states are fetched at once: 8 (189,272 tokens x 16 x 128: 99 us, with 4 123), or 4 where there are no more
-// and fewer registers let more CTAs run at once (8 x 2000 x 16 x 128: 10 us, with 8 13).
+// U local states are fetched at once: 8 where the CTAs do not fill the GPU twice over (33,272 tokens x 16 x 128 forward:
+// 45 us, with 4 51; 4 x 8192 x 16 x 64: 11, with 4 12), else 4, whose fewer registers let more CTAs run at once
+// (4 x 8192 x 16 x 128: 40 us, with 8 43; 8 prompts of up to 2000: 18.5, with 8 22; 33,272 tokens backward: 86, with 8 93).
 template <int D, bool ONE, int U>
 __global__ void __launch_bounds__(128) lin_tc_scan_kernel(const __grid_constant__ LinScanSets sets) {
   constexpr int kPerSet = D * D / 8 / 128;
@@ -638,16 +639,17 @@ int64_t linear_tc_most_states(const Dims& d) {
 cudaError_t launch_linear_tc_local(const Dims& d, const LinLocalSets& a, uint32_t* status, cudaStream_t s) {
   return d.dk == 128 ? local<128>(d, a, status, s) : local<64>(d, a, status, s);
 }
-template <int D, int U>
-static void scan(const Dims& d, const LinScanSets& a, cudaStream_t s) {
-  const auto kernel = a.n == 1 ? lin_tc_scan_kernel<D, true, U> : lin_tc_scan_kernel<D, false, U>;
-  kernel<<<dim3(D * D / 8 / 128 * a.n, d.H, d.B), 128, 0, s>>>(a);
+template <int D>
+static cudaError_t scan(const Dims& d, const LinScanSets& a, cudaStream_t s) {
+  const dim3 grid(D * D / 8 / 128 * a.n, d.H, d.B);
+  const bool four = a.set[0].n_seg <= 4 || (int64_t)grid.x * d.H * d.B >= 2 * 148;
+  const auto kernel = a.n == 1 ? (four ? lin_tc_scan_kernel<D, true, 4> : lin_tc_scan_kernel<D, true, 8>)
+                               : (four ? lin_tc_scan_kernel<D, false, 4> : lin_tc_scan_kernel<D, false, 8>);
+  kernel<<<grid, 128, 0, s>>>(a);
+  return cudaGetLastError();
 }
 cudaError_t launch_linear_tc_scan(const Dims& d, const LinScanSets& a, cudaStream_t s) {
-  const bool few = a.set[0].n_seg <= 4;
-  if (d.dk == 128) few ? scan<128, 4>(d, a, s) : scan<128, 8>(d, a, s);
-  else few ? scan<64, 4>(d, a, s) : scan<64, 8>(d, a, s);
-  return cudaGetLastError();
+  return d.dk == 128 ? scan<128>(d, a, s) : scan<64>(d, a, s);
 }
 cudaError_t launch_linear_tc_map(const Dims& d, const LinMapSets& a, uint32_t* status, cudaStream_t s) {
   return d.dk == 128 ? map<128>(d, a, status, s) : map<64>(d, a, status, s);
