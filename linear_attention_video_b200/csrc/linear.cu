@@ -51,7 +51,9 @@ __global__ void __launch_bounds__(128) lin_scan_kernel(const __grid_constant__ L
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.initial) S = *reinterpret_cast<const float4*>(a.initial + bh * dd + e);
   float* p = a.states + bh * a.n_seg * dd + e;
-  constexpr int U = ONE ? 8 : 4;   // states fetched at once (33,272 x 16 x 128: 86 us, 4 102; two sets 178, 8 285)
+  // States fetched at once.  33,272 x 16 x 128: 6 92 us, 4 104, 8 197; 16 x 64: 49, 62, 57; 2 x 16,000 x 16 x 128: 84, 83,
+  // 134; two sets of 33,272 x 16 x 128: 4 177, 8 285.
+  constexpr int U = ONE ? 6 : 4;
   for (int c0 = 0; c0 < a.n_seg; c0 += U) {
     float4 loc[U];
 #pragma unroll
