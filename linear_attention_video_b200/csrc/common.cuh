@@ -138,7 +138,7 @@ struct LinScanSets { LinScanArgs set[2]; int n; };
 struct LinMapArgs {
   const void *a, *b, *c;
   void* out;
-  const float *states, *initial;   // what enters each segment; with one segment, `initial` itself
+  const float *states, *initial;   // what enters each segment; of fp32 problems with one segment, `initial` itself
   const float* log_decay;
   const int32_t* lengths;
   int64_t N;

@@ -80,7 +80,8 @@ template <int V> __device__ __forceinline__ void load_par(const float* p, int c,
   }
 }
 
-// Two fp32 operations in one instruction: half the issue slots, which is what holds the bf16 rows.
+// Two fp32 operations in one instruction: half the issue slots.  With them the backward pass of bf16 rows issues in 55%
+// of its cycles and waits for memory: a row prefetched in registers is 32 KB in flight per SM.
 __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
   asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
       : "+f"(x), "+f"(y) : "f"(a), "f"(b));
@@ -177,6 +178,8 @@ template <int G> struct Shape {
   static constexpr int groups = threads / G;
 };
 // Resident threads per SM that registers must allow.  Backward: 640 would spill (33,272 x 2048 bf16: 123 us against 83).
+// Rows of more than 8192 columns take 1024 threads, whose 64 registers each do spill: 4000 x 16,384 bf16 backward 213 us
+// (1.85 TB/s; 10,000 x 8192: 112 us, 4.4 TB/s), fp32 402 us.
 constexpr int kFwdThreads = 1024, kBwdThreads = 512;
 constexpr int ctas_of(int threads, int resident) { return threads < resident ? resident / threads : 1; }
 
@@ -466,9 +469,9 @@ cudaError_t fwd(const NormFwdArgs& a, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-// Backward: 16 elements of a row per lane and one row at a time (33,272 x 2048 bf16: 80 us; 8 and two rows 83 us, the
-// reductions then cost a third of the instructions; 16 and two rows 151 us, out of registers).  Scalar accesses take
-// 8 and two rows (2047 columns: 116 us against 160).
+// Backward: 16 elements of a row per lane and one row at a time (33,272 x 2048 bf16: 83 us with the sums' 5; 8 and two
+// rows 84 us, the reductions then cost a third of the instructions; 16 and two rows 137 us, out of registers).  Scalar
+// accesses take 8 and two rows (2047 columns: 116 us against 163).
 int lanes_for(int cols, int e) {
   int g = 8;
   while (g < 1024 && g * e < cols) g *= 2;

@@ -11,8 +11,8 @@
 // What is rounded: an output, once, to bf16.  A decayed score and a state that enters a segment go into their products
 // with c and a as two bf16 terms, which leaves 2^-16 of each (a state is an fp32 argument and the past of every later
 // token, and the single-token call reads it in fp32).  The error against fp64 is that of rounding the exact outputs,
-// 1.66e-3 of their norm at random.  One term each would give 2.35e-3; 33,272 x 16 x 128 forward takes 292 us as it is,
-// 270 with scores of one term, 278 with states of one, 258 with both.  The states stay fp32 from segment to segment, and
+// 1.66e-3 of their norm at random.  One term each would give 2.35e-3; 33,272 x 16 x 128 forward took 292 us as it
+// is, 270 with scores of one term, 278 with states of one, 258 with both (in segments of 512 tokens).  The states stay fp32 from segment to segment, and
 // the sums that become a state are taken of three bf16 terms (24 bits), because states are fp32 results.
 // All sums are fp32.
 //
@@ -619,10 +619,10 @@ cudaError_t map(const Dims& d, const LinMapSets& a, uint32_t* status, cudaStream
 }  // namespace
 
 // Tokens per segment.  A longer one costs the map more tiles of scores per row, a shorter one costs states.  33,272
-// tokens x 16 x 128: forward 296 us with 256, 292 with 512, 353 with 1024; backward 684, 714 and 930.  8 ragged prompts of
-// up to 2000: 128 us with 256 and 123 with 512, their backward pass 281 and 284; 4 x 8192 x 16 x 64: 169 us with 256 and 188 with
-// 512, backward 467 and 540.
-// Where the segments would not give every SM its two CTAs of the local sums, shorter ones take less time in a row.
+// tokens x 16 x 128: forward 296 us with 256, 292 with 512, 353 with 1024; backward 684, 714 and 930.  8 ragged prompts
+// of up to 2000: 128 us with 256 and 123 with 512, their backward pass 281 and 284; 4 x 8192 x 16 x 64: 169 us with 256
+// and 188 with 512, backward 467 and 540.  Where the segments would not give every SM its two CTAs of the local sums,
+// shorter ones take less time in a row.
 int linear_tc_segment(const Dims& d) {
   int seg = kMaxSeg;
   while (seg > TM && (int64_t)d.B * d.H * ((d.N + seg - 1) / seg) < 2 * 148) seg /= 2;

@@ -11,7 +11,7 @@ namespace kda {
 namespace {
 
 // lam^n; 1 at n = 0 whatever the decay.  Only whole n >= 0 occur, so nothing overflows however fast a head forgets;
-// the fp32 error of n log lam, 2^-25 |n log lam|, is largest beside e^-1.
+// the fp32 error of n log lam, at most 2^-24 |n log lam|, is largest beside e^-1.
 __device__ __forceinline__ float decay_pow(float log_decay, int64_t n) {
   return n == 0 ? 1.f : expf((float)n * log_decay);
 }
