@@ -11,10 +11,10 @@
 // What is rounded: an output, once, to bf16.  A decayed score and a state that enters a segment go into their products
 // with c and a as two bf16 terms, which leaves 2^-16 of each (a state is an fp32 argument and the past of every later
 // token, and the single-token call reads it in fp32).  The error against fp64 is that of rounding the exact outputs,
-// 1.66e-3 of their norm at random.  One term each would give 2.35e-3; 33,272 x 16 x 128 forward took 292 us as it
-// is, 270 with scores of one term, 278 with states of one, 258 with both (in segments of 512 tokens).  The states stay fp32 from segment to segment, and
-// the sums that become a state are taken of three bf16 terms (24 bits), because states are fp32 results.
-// All sums are fp32.
+// 1.66e-3 of their norm at random.  One term each would give 2.35e-3; 33,272 x 16 x 128 forward took 292 us as it is,
+// 270 with scores of one term, 278 with states of one, 258 with both (in segments of 512 tokens).  The states stay fp32
+// from segment to segment, and the sums that become a state are taken of three bf16 terms (24 bits), because states are
+// fp32 results.  All sums are fp32.
 //
 // State images.  Between scan and map a state is two bf16 matrices, its first and second terms, in the
 // 128-byte-swizzled panels that the tensor core reads, so a CTA fetches each with one bulk copy.  Of a segment's fp32
